@@ -25,6 +25,8 @@ STATUS = {
 FLAG_BAD_PAGE_ID = 1
 FLAG_BAD_STATE = 2
 FLAG_TIMEOUT = 4
+FLAG_BAD_TREE = 8
+MAX_DRAFT = 64
 PAGE_BLOCK_BYTES = 1536  # group size 32
 
 
@@ -81,6 +83,16 @@ _SIGS = {
     "oscar_decode_attn_shared_prefix": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int32, _P, ctypes.c_int32, _P]),
     "oscar_decode_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P]),
     "oscar_decode_step_host": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P]),
+    "oscar_tree_attn_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
+    "oscar_tree_attn": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P,
+                                       ctypes.c_size_t, _P]),
+    "oscar_commit_draft": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P]),
+    "oscar_verify_draft": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                          _P, _P, _P, _P, _P]),
+    "oscar_rope_turns": (ctypes.c_int, [_P, ctypes.c_int32, _P]),
+    "oscar_qkv_norm_rope": (ctypes.c_int, [_P, ctypes.c_int64, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                           ctypes.c_float, _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_int32, _P]),
     "oscar_calibration_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "oscar_calibration_covariances": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                                      ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -168,6 +180,29 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _arg(name, t, dtype, shape):
+    """Device pointer of a tensor argument, checked: CUDA, dtype, shape, dense row-major."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor" % name)
+    return _ptr(t)
+
+
+def _on_device(*tensors):
+    """Context manager making the tensors' device current; they must share one."""
+    import torch
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError("tensors on different devices: %s" % sorted(map(str, devs)))
+    dev = devs.pop()
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors, got %s" % dev)
+    return torch.cuda.device(dev)
+
+
 def _event(ev):
     """Raw cudaEvent_t of a torch.cuda.Event (recorded once so that it exists)."""
     if ev is None:
@@ -181,6 +216,59 @@ def _stream(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def verify_draft(probs, tokens, parent, u_accept, u_sample, path, n_path, next_token, draft_probs=None,
+                 draft_len=None, err_flags=None, stream=None):
+    """oscar_verify_draft: the accepted path of every request's tree of drafted tokens
+    (path [batch, n_draft], n_path [batch]) and the token after it (next_token [batch])."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    if probs.dim() != 3:
+        raise ValueError("probs: expected [batch, n_draft, vocab], got %s" % list(probs.shape))
+    b, t, v = probs.shape
+    with _on_device(probs, tokens, parent, u_accept, u_sample, path, n_path, next_token, draft_probs, draft_len,
+                    err_flags):
+        _check(lib().oscar_verify_draft(
+            _arg("probs", probs, f32, (b, t, v)), _arg("draft_probs", draft_probs, f32, (b, t, v)),
+            _arg("tokens", tokens, i32, (b, t)), _arg("parent", parent, i32, (b, t)),
+            _arg("draft_len", draft_len, i32, (b,)), _arg("u_accept", u_accept, f32, (b, t)),
+            _arg("u_sample", u_sample, f32, (b,)), b, t, v, _arg("path", path, i32, (b, t)),
+            _arg("n_path", n_path, i32, (b,)), _arg("next_token", next_token, i32, (b,)), _ptr(err_flags),
+            _stream(stream)))
+
+
+def rope_turns(inv_freq):
+    """The frequency table of qkv_norm_rope: inv_freq (radians per position, one per pair) as
+    64-bit fractions of a turn, an int64 CPU tensor (the bits of oscar_rope_turns' uint64)."""
+    import numpy as np
+    import torch
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    out = np.empty(f.shape, dtype=np.uint64)
+    _check(lib().oscar_rope_turns(f.ctypes.data_as(_P), f.size, out.ctypes.data_as(_P)))
+    return torch.from_numpy(out.view(np.int64))
+
+
+def qkv_norm_rope(qkv, pos, turns, q, k, v, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None):
+    """oscar_qkv_norm_rope: the rows of a fused projection qkv [n, (Hq + 2 Hkv) * 128] (rows may be
+    padded) split into q [n, Hq, 128] and k, v [n, Hkv, 128], with the norm of every q and k head
+    (when the weights are given) and the rotation by pos [n]; turns from rope_turns."""
+    import torch
+    bf = torch.bfloat16
+    n, hq, hkv = q.shape[0], q.shape[1], k.shape[1]
+    width = (hq + 2 * hkv) * 128
+    if qkv.dtype != bf or tuple(qkv.shape) != (n, width) or qkv.stride(1) != 1 or (n > 1 and qkv.stride(0) < width):
+        raise ValueError("qkv: expected bf16 rows [%d, %d] with dense columns, got %s %s, strides %s"
+                         % (n, width, qkv.dtype, list(qkv.shape), tuple(qkv.stride())))
+    if turns.dim() != 1:
+        raise ValueError("turns: expected [rotary_dim / 2]")
+    with _on_device(qkv, pos, turns, q, k, v, q_weight, k_weight):
+        _check(lib().oscar_qkv_norm_rope(
+            ctypes.c_void_p(qkv.data_ptr()), qkv.stride(0) if n > 1 else width,
+            _arg("pos", pos, torch.int32, (n,)), _arg("turns", turns, torch.int64, turns.shape), 2 * turns.shape[0],
+            1 if interleaved else 0, _arg("q_weight", q_weight, bf, (128,)), _arg("k_weight", k_weight, bf, (128,)),
+            eps, _arg("q", q, bf, (n, hq, 128)), _arg("k", k, bf, (n, hkv, 128)), _arg("v", v, bf, (n, hkv, 128)),
+            n, hq, hkv, _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -273,6 +361,36 @@ class Context:
         staging buffer d_qkv, output o (device) copied to host memory h_o."""
         _check(lib().oscar_decode_step_host(self.handle, _ptr(page_table), _ptr(state), _ptr(h_qkv), _ptr(d_qkv),
                                             _ptr(o), _ptr(h_o), batch, _stream(stream)), self.handle)
+
+    def tree_attn_workspace_bytes(self, batch, n_draft):
+        return lib().oscar_tree_attn_workspace_bytes(self.handle, batch, n_draft)
+
+    def tree_attn(self, q, k, v, parent, page_table, state, o, batch, n_draft, workspace, draft_len=None, stream=None):
+        """oscar_tree_attn: attention of n_draft drafted tokens per request (a tree given by
+        `parent`) over the cache and their own ancestors. workspace: a uint8 CUDA tensor of at
+        least tree_attn_workspace_bytes(batch, n_draft) bytes."""
+        import torch
+        c, bf = self.cfg, torch.bfloat16
+        with _on_device(q, k, v, parent, page_table, state, o, workspace, draft_len):
+            _check(lib().oscar_tree_attn(
+                self.handle, _arg("q", q, bf, (batch, n_draft, c.num_q_heads, 128)),
+                _arg("k", k, bf, (batch, n_draft, c.num_kv_heads, 128)),
+                _arg("v", v, bf, (batch, n_draft, c.num_kv_heads, 128)),
+                _arg("parent", parent, torch.int32, (batch, n_draft)),
+                _arg("draft_len", draft_len, torch.int32, (batch,)), _ptr(page_table), _ptr(state),
+                _arg("o", o, bf, (batch, n_draft, c.num_q_heads, 128)), batch, n_draft, _ptr(workspace),
+                workspace.numel() * workspace.element_size(), _stream(stream)), self.handle)
+
+    def commit_draft(self, page_table, state, k, v, path, n_path, batch, n_draft, stream=None):
+        """oscar_commit_draft: request b appends rows path[b, :n_path[b]] of k and v [batch, n_draft,
+        Hkv, 128] to the cache."""
+        import torch
+        c, bf, i32 = self.cfg, torch.bfloat16, torch.int32
+        with _on_device(page_table, state, k, v, path, n_path):
+            _check(lib().oscar_commit_draft(
+                self.handle, _ptr(page_table), _ptr(state), _arg("k", k, bf, (batch, n_draft, c.num_kv_heads, 128)),
+                _arg("v", v, bf, (batch, n_draft, c.num_kv_heads, 128)), _arg("path", path, i32, (batch, n_draft)),
+                _arg("n_path", n_path, i32, (batch,)), batch, n_draft, _stream(stream)), self.handle)
 
     def decode_splits(self, batch):
         s = ctypes.c_int32()

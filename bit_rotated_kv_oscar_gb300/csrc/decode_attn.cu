@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "oscar_internal.cuh"
+#include "int2_page.cuh"
 #include "token_quant.cuh"
 
 namespace oscar {
@@ -52,22 +53,6 @@ constexpr int kStageBytes = kWarps * kStages * kBlockBytes;   // 48 KB with 4 st
 static_assert((kStages & (kStages - 1)) == 0 && kStages >= 2, "page ring depth must be a power of two");
 constexpr int kMaxWindow = 1024;                                // sink + recent limit
 constexpr int kWinChunk = kWindowChunkMax;                      // window tokens per CTA, at most
-
-// factor of a code read from slot i (see the file comment)
-__host__ __device__ constexpr float slot_factor(int i) {
-  return i <= 4 ? (float)(1 << (2 * i)) : (float)(1 << (2 * (i - 5)));
-}
-
-// w: a code word, wh = w >> 10 (computed once per word, shared by slots 5..7)
-template <int I>
-__device__ __forceinline__ uint32_t slot_bits(uint32_t w, uint32_t wh) {
-  if constexpr (I <= 4) {
-    return w & (0x00030003u << (2 * I));
-  } else {
-    return wh & (0x00030003u << (2 * (I - 5)));
-  }
-}
-__device__ __forceinline__ uint4 shr10(uint4 w) { return make_uint4(w.x >> 10, w.y >> 10, w.z >> 10, w.w >> 10); }
 
 // d += a b (no side effects: not volatile, so the compiler may interleave
 // independent products with the arithmetic around them)
@@ -610,36 +595,6 @@ __device__ __forceinline__ void page_values(const uint8_t* sb, int lane, uint32_
   if (gid < NG) mz = *reinterpret_cast<const uint2*>(sb + vbase + 16 * (4 * gid + tig) + 8);
   const uint32_t za0 = mz.x, za2 = mz.y;
   mma16816(oz, za0, 0u, za2, 0u, P01, P23);
-}
-
-// bits t of the tokens t in [0, 16) of a page at position pos that lie in [lo, hi)
-__device__ __forceinline__ uint32_t page_token_bits(bool ok, int pos, int lo, int hi) {
-  const int a = max(lo - pos, 0), e = min(hi - pos, kPage);
-  return (ok && e > a) ? (((1u << (e - a)) - 1u) << a) : 0u;
-}
-
-// zero the value scales and zeros of the tokens of two staged pages whose bit in
-// `valid` is clear (bit t: page A token t, bit 16 + t: page B token t); lane:
-// page lane / 16, 16-byte chunk c = 4 g + bb of the value metadata, whose 32-bit
-// word w holds tokens 8 (w % 2) + 2 bb and + 1 (scales for w < 2, zeros after)
-template <int NG>
-__device__ __forceinline__ void zero_masked_value_meta(uint8_t* sbA, uint8_t* sbB, uint32_t valid, int lane) {
-  const int c = lane & 15;
-  if (c >= 4 * NG) return;  // NG groups: 4 NG chunks
-  const uint32_t vpage = (lane >> 4) ? (valid >> 16) : (valid & 0xffffu);
-  uint4* chunk = reinterpret_cast<uint4*>(((lane >> 4) ? sbB : sbA) + vscale_off(NG, 0, 0) + 16 * c);
-  uint32_t keep[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int tw = 8 * (w & 1) + 2 * (c & 3);
-    keep[w] = (((vpage >> tw) & 1u) ? 0x0000ffffu : 0u) | (((vpage >> (tw + 1)) & 1u) ? 0xffff0000u : 0u);
-  }
-  uint4 x = *chunk;
-  x.x &= keep[0];
-  x.y &= keep[1];
-  x.z &= keep[2];
-  x.w &= keep[3];
-  *chunk = x;
 }
 
 // INT2 positions [lo, hi) of KV head h, the split-th of nsplits slices of its

@@ -5,6 +5,8 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
+#include <initializer_list>
 #include <new>
 #include <string>
 #include <vector>
@@ -29,8 +31,10 @@ struct oscar_ctx {
   float* clip_V = nullptr;
   float* pv_scale = nullptr;
   uint8_t* images = nullptr;    // per KV head: R_K hi/lo, R_V hi/lo as swizzled bf16 tensor-core operands
+  __half* rv16 = nullptr;       // R_V in fp16 (the tree attention's un-rotation operand)
   uint32_t* qrec = nullptr;
   float* part = nullptr;
+  uint32_t* tickets = nullptr;  // per request of a commit: CTAs that have read its state
   uint32_t* flags = nullptr;    // [0] error flags, [1] append ticket counter
   int max_splits = 0;
   bool loaded = false;
@@ -206,6 +210,8 @@ void oscar_destroy(oscar_ctx* ctx) {
   cudaFree(ctx->clip_V);
   cudaFree(ctx->pv_scale);
   cudaFree(ctx->images);
+  cudaFree(ctx->rv16);
+  cudaFree(ctx->tickets);
   cudaFree(ctx->qrec);
   cudaFree(ctx->part);
   cudaFree(ctx->flags);
@@ -233,6 +239,9 @@ int oscar_create(const oscar_config* cfg, oscar_ctx** out) {
   if (e == cudaSuccess) e = dalloc(&ctx->clip_V, hkv * sizeof(float));
   if (e == cudaSuccess) e = dalloc(&ctx->pv_scale, hkv * sizeof(float));
   if (e == cudaSuccess) e = dalloc(&ctx->images, (size_t)hkv * prefill_image_bytes());
+  if (e == cudaSuccess) e = dalloc(&ctx->rv16, rbytes / 2);
+  if (e == cudaSuccess) e = dalloc(&ctx->tickets, cfg->max_batch * sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaMemset(ctx->tickets, 0, cfg->max_batch * sizeof(uint32_t));
   if (e == cudaSuccess) {
     ctx->max_splits = auto_splits(ctx, cfg->max_batch);
     for (int b = 1; b < cfg->max_batch; ++b) {
@@ -302,7 +311,10 @@ int oscar_load_rotations(oscar_ctx* ctx, const float* R_K, const float* R_V, con
     rotation_images(R_K + (size_t)h * m, false, base, base + m);
     rotation_images(R_V + (size_t)h * m, ctx->cfg.fold_rv != 0, base + 2 * m, base + 3 * m);
   }
+  std::vector<__half> rv16(n);
+  for (size_t i = 0; i < n; ++i) rv16[i] = __float2half_rn(R_V[i]);
   cudaError_t e = cudaMemcpy(ctx->images, img.data(), img.size() * sizeof(uint16_t), cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaMemcpy(ctx->rv16, rv16.data(), n * sizeof(__half), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(ctx->R_K, R_K, n * sizeof(float), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(ctx->R_V, R_V, n * sizeof(float), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(ctx->R_VT, rvt.data(), n * sizeof(float), cudaMemcpyHostToDevice);
@@ -579,6 +591,221 @@ int oscar_decode_step_host(oscar_ctx* ctx, const int32_t* page_table, oscar_seq_
     if (e != cudaSuccess) return cuda_fail(ctx, e, "decode_step_host: output copy");
   }
   return OSCAR_OK;
+}
+
+// Launch shapes of a tree-attention call, the same for the workspace query and the call.
+struct TreePlan {
+  int rows, tile_rows, col_tiles, row_tiles, win_slots, splits;
+  size_t rec_bytes, part_bytes;
+};
+static TreePlan tree_plan(const oscar_ctx* ctx, int batch, int nodes) {
+  TreePlan t{};
+  const int hkv = ctx->cfg.num_kv_heads;
+  t.rows = nodes * (ctx->cfg.num_q_heads / hkv);
+  t.tile_rows = t.rows <= 16 ? 16 : 32;
+  t.col_tiles = (t.rows + t.tile_rows - 1) / t.tile_rows;
+  t.row_tiles = (t.rows + 31) / 32;
+  t.win_slots = (ctx->cfg.sink + ctx->cfg.recent + nodes + kTreeWindowChunk - 1) / kTreeWindowChunk;
+  // one wave of CTAs together with the BF16 ones, at most kSplitPages pages per CTA
+  const int64_t units = (int64_t)batch * hkv * t.col_tiles, pages = ctx->cfg.max_pages_per_seq;
+  const int64_t ctas = (t.tile_rows == 16 ? 2 : 1) * (int64_t)ctx->num_sms;
+  int64_t s = std::max((ctas - units * t.win_slots) / units, (pages + kSplitPages - 1) / kSplitPages);
+  s = std::min<int64_t>(s, (pages + 7) / 8);   // >= 8 pages per split: one per warp
+  if (ctx->cfg.num_splits > 0) s = ctx->cfg.num_splits;
+  t.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 256));
+  t.rec_bytes = ((size_t)batch * hkv * t.row_tiles * kTreeRecWords * 4 + 255) / 256 * 256;
+  t.part_bytes = (size_t)batch * hkv * (t.win_slots + t.splits) * t.rows * kPartFloats * sizeof(float);
+  return t;
+}
+
+// a call of the drafted-token operators on a context: its state and arguments
+static int check_draft_call(oscar_ctx* ctx, const char* what, int32_t batch, int32_t nodes) {
+  const std::string w = what;
+  if (!ctx->loaded) return fail(ctx, OSCAR_ERR_NOT_LOADED, w + ": rotations not loaded");
+  if (!ctx->pool) return fail(ctx, OSCAR_ERR_NOT_BOUND, w + ": no cache bound");
+  if (batch < 1) return fail(ctx, OSCAR_ERR_INVALID_ARG, w + ": batch >= 1");
+  if (batch > ctx->cfg.max_batch) return fail(ctx, OSCAR_ERR_OUT_OF_RANGE, w + ": batch exceeds max_batch");
+  if (nodes < 1) return fail(ctx, OSCAR_ERR_INVALID_ARG, w + ": n_draft >= 1");
+  if (nodes > kTreeNodes) return fail(ctx, OSCAR_ERR_UNSUPPORTED, w + ": n_draft must not exceed 64");
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, what);
+  if (dev != ctx->device) return fail(ctx, OSCAR_ERR_INVALID_ARG, w + ": the context belongs to another device");
+  return OSCAR_OK;
+}
+
+static bool aligned16(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return true;
+}
+
+size_t oscar_tree_attn_workspace_bytes(const oscar_ctx* ctx, int32_t batch, int32_t n_draft) {
+  if (!ctx || batch < 1 || batch > ctx->cfg.max_batch || n_draft < 1 || n_draft > kTreeNodes) return 0;
+  const TreePlan t = tree_plan(ctx, batch, n_draft);
+  return t.rec_bytes + t.part_bytes;
+}
+
+int oscar_tree_attn(oscar_ctx* ctx, const void* q, const void* k, const void* v, const int32_t* parent,
+                    const int32_t* draft_len, const int32_t* page_table, const oscar_seq_state* state, void* o,
+                    int32_t batch, int32_t n_draft, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ctx) return OSCAR_ERR_INVALID_ARG;
+  if (!q || !k || !v || !parent || !page_table || !state || !o || !workspace)
+    return fail(ctx, OSCAR_ERR_INVALID_ARG, "tree_attn: null pointer");
+  const int st = check_draft_call(ctx, "tree_attn", batch, n_draft);
+  if (st != OSCAR_OK) return st;
+  if (!aligned16({q, k, v, o, workspace}))
+    return fail(ctx, OSCAR_ERR_INVALID_ARG, "tree_attn: q, k, v, o and workspace must be 16-byte aligned");
+  const TreePlan t = tree_plan(ctx, batch, n_draft);
+  if (workspace_bytes < t.rec_bytes + t.part_bytes)
+    return fail(ctx, OSCAR_ERR_OUT_OF_RANGE, "tree_attn: workspace smaller than oscar_tree_attn_workspace_bytes");
+  TreeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.parent = parent;
+  p.draft_len = draft_len;
+  p.page_table = page_table;
+  p.pt_stride = ctx->cfg.max_pages_per_seq;
+  p.state = state;
+  p.pool = ctx->pool;
+  p.num_pages = ctx->num_pages;
+  p.window = ctx->window;
+  p.images = ctx->images;
+  p.rv16 = ctx->rv16;
+  p.pv_scale = ctx->pv_scale;
+  p.qrec = static_cast<uint32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + t.rec_bytes);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.num_q_heads = ctx->cfg.num_q_heads;
+  p.num_kv_heads = ctx->cfg.num_kv_heads;
+  p.gqa = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads;
+  p.sink = ctx->cfg.sink;
+  p.recent = ctx->cfg.recent;
+  p.ngroups = kHeadDim / ctx->cfg.group_size;
+  p.fold_rv = ctx->cfg.fold_rv;
+  p.max_batch = ctx->cfg.max_batch;
+  p.batch = batch;
+  p.nodes = n_draft;
+  p.tile_rows = t.tile_rows;
+  p.col_tiles = t.col_tiles;
+  p.row_tiles = t.row_tiles;
+  p.win_slots = t.win_slots;
+  p.splits = t.splits;
+  p.scale_log2 = ctx->cfg.softmax_scale * 1.4426950408889634f;
+  p.err_flags = ctx->flags;
+  const cudaError_t e = launch_tree_attn(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? OSCAR_OK : cuda_fail(ctx, e, "tree_attn launch");
+}
+
+int oscar_commit_draft(oscar_ctx* ctx, const int32_t* page_table, oscar_seq_state* state, const void* k,
+                       const void* v, const int32_t* path, const int32_t* n_path, int32_t batch, int32_t n_draft,
+                       void* stream) {
+  if (!ctx) return OSCAR_ERR_INVALID_ARG;
+  if (!page_table || !state || !k || !v || !path || !n_path)
+    return fail(ctx, OSCAR_ERR_INVALID_ARG, "commit_draft: null pointer");
+  const int st = check_draft_call(ctx, "commit_draft", batch, n_draft);
+  if (st != OSCAR_OK) return st;
+  if (!aligned16({k, v})) return fail(ctx, OSCAR_ERR_INVALID_ARG, "commit_draft: k and v must be 16-byte aligned");
+  CommitParams p{};
+  p.page_table = page_table;
+  p.pt_stride = ctx->cfg.max_pages_per_seq;
+  p.state = state;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.path = path;
+  p.count = n_path;
+  p.pool = ctx->pool;
+  p.num_pages = ctx->num_pages;
+  p.window = ctx->window;
+  p.R_K = ctx->R_K;
+  p.R_V = ctx->R_V;
+  p.clip_K = ctx->clip_K;
+  p.clip_V = ctx->clip_V;
+  p.num_kv_heads = ctx->cfg.num_kv_heads;
+  p.sink = ctx->cfg.sink;
+  p.recent = ctx->cfg.recent;
+  p.ngroups = kHeadDim / ctx->cfg.group_size;
+  p.fold_rv = ctx->cfg.fold_rv;
+  p.max_batch = ctx->cfg.max_batch;
+  p.batch = batch;
+  p.nodes = n_draft;
+  p.tickets = ctx->tickets;
+  p.err_flags = ctx->flags;
+  const cudaError_t e = launch_commit_draft(p, ctx->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? OSCAR_OK : cuda_fail(ctx, e, "commit_draft launch");
+}
+
+int oscar_verify_draft(const float* probs, const float* draft_probs, const int32_t* tokens, const int32_t* parent,
+                       const int32_t* draft_len, const float* u_accept, const float* u_sample, int32_t batch,
+                       int32_t n_draft, int32_t vocab, int32_t* path, int32_t* n_path, int32_t* next_token,
+                       uint32_t* err_flags, void* stream) {
+  if (!probs || !tokens || !parent || !u_accept || !u_sample || !path || !n_path || !next_token || batch < 1 ||
+      n_draft < 1 || vocab < 1)
+    return OSCAR_ERR_INVALID_ARG;
+  if (n_draft > kTreeNodes || vocab > (1 << 18)) return OSCAR_ERR_UNSUPPORTED;
+  if (batch > (1 << 20)) return OSCAR_ERR_OUT_OF_RANGE;
+  VerifyParams p{};
+  p.probs = probs;
+  p.draft_probs = draft_probs;
+  p.tokens = tokens;
+  p.parent = parent;
+  p.draft_len = draft_len;
+  p.u_accept = u_accept;
+  p.u_sample = u_sample;
+  p.path = path;
+  p.n_path = n_path;
+  p.next_token = next_token;
+  p.batch = batch;
+  p.nodes = n_draft;
+  p.vocab = vocab;
+  p.err_flags = err_flags;
+  return launch_verify_draft(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+int oscar_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
+  if (!inv_freq || !turns || n < 1) return OSCAR_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (!std::isfinite(inv_freq[i])) return OSCAR_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i) {
+    double x = inv_freq[i] / 6.283185307179586476925286766559;   // turns per position
+    x -= std::floor(x);                                            // whole turns do nothing
+    const double hi = std::floor(x * 4294967296.0);
+    const double lo = std::floor((x * 4294967296.0 - hi) * 4294967296.0);
+    turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+  }
+  return OSCAR_OK;
+}
+
+int oscar_qkv_norm_rope(const void* qkv, int64_t row_stride, const int32_t* pos, const uint64_t* turns,
+                        int32_t rotary_dim, int32_t interleaved, const void* q_weight, const void* k_weight, float eps,
+                        void* q, void* k, void* v, int32_t n_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        void* stream) {
+  if (n_tokens == 0) return OSCAR_OK;
+  if (!qkv || !pos || !turns || !q || !k || !v || n_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
+      (q_weight == nullptr) != (k_weight == nullptr) || !(eps >= 0.f) || isinf(eps))
+    return OSCAR_ERR_INVALID_ARG;
+  if (rotary_dim < 16 || rotary_dim > kHeadDim || rotary_dim % 16) return OSCAR_ERR_UNSUPPORTED;
+  const int64_t width = ((int64_t)num_q_heads + 2 * (int64_t)num_kv_heads) * kHeadDim;
+  if (width > INT32_MAX || row_stride < width || row_stride % 8) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned16({qkv, q, k, v, q_weight, k_weight}) || (reinterpret_cast<uintptr_t>(turns) & 7)) return OSCAR_ERR_INVALID_ARG;
+  RopeParams p{};
+  p.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  p.row_stride = row_stride;
+  p.tokens = n_tokens;
+  p.pos = pos;
+  p.turns = reinterpret_cast<const unsigned long long*>(turns);
+  p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+  p.eps = eps;
+  p.rotary = rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.q = static_cast<__nv_bfloat16*>(q);
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  return launch_qkv_norm_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 int oscar_error_flags(oscar_ctx* ctx, uint32_t* flags, int32_t clear) {

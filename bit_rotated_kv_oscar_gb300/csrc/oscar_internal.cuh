@@ -163,6 +163,89 @@ __host__ __device__ __forceinline__ int total_slots(const DecodeParams& p) {
   return p.win_slots + p.prefix_splits + p.splits + p.step_slots;
 }
 
+// A tree of drafted tokens per request (oscar_tree_attn): `nodes` rows of q, k, v
+// and o per request, `nodes * gqa` query rows per KV head.
+constexpr int kTreeNodes = 64;          // nodes per request, at most
+constexpr int kTreeWindowChunk = 128;   // BF16 tokens (sink, ring, tree) per CTA
+constexpr int kTreeRecWords = 2192;     // query record of 32 query rows (see tree_attn.cu)
+struct TreeParams {
+  const __nv_bfloat16* q;   // [B][nodes][Hq][128]
+  const __nv_bfloat16* k;   // [B][nodes][Hkv][128]
+  const __nv_bfloat16* v;
+  const int32_t* parent;    // [B][nodes]
+  const int32_t* draft_len; // [B] or null: every request uses all nodes
+  const int32_t* page_table;
+  int32_t pt_stride;
+  const oscar_seq_state* state;
+  const uint8_t* pool;
+  int64_t num_pages;
+  const __nv_bfloat16* window;
+  const uint8_t* images;    // [Hkv][4][32 KiB]: R_K hi, R_K lo, ... (bf16, swizzled)
+  const __half* rv16;       // [Hkv][128][128] R_V, row-major
+  const float* pv_scale;    // [Hkv]
+  uint32_t* qrec;           // [B][Hkv][row_tiles][kTreeRecWords]
+  float* part;              // [B][Hkv][win_slots + splits][nodes * gqa][kPartFloats]
+  __nv_bfloat16* o;         // [B][nodes][Hq][128]
+  int32_t num_q_heads, num_kv_heads, gqa, sink, recent, ngroups, fold_rv, max_batch, batch, nodes;
+  int32_t tile_rows;        // query rows per attention CTA: 16 or 32
+  int32_t col_tiles;        // tiles of tile_rows rows
+  int32_t row_tiles;        // records of 32 rows
+  int32_t win_slots, splits;
+  float scale_log2;
+  uint32_t* err_flags;
+};
+
+// accepted rows of a draft appended to the cache (oscar_commit_draft)
+struct CommitParams {
+  const int32_t* page_table;
+  int32_t pt_stride;
+  oscar_seq_state* state;
+  const __nv_bfloat16* k;   // [B][nodes][Hkv][128]
+  const __nv_bfloat16* v;
+  const int32_t* path;      // [B][nodes]
+  const int32_t* count;     // [B]
+  uint8_t* pool;
+  int64_t num_pages;
+  __nv_bfloat16* window;
+  const float* R_K;
+  const float* R_V;
+  const float* clip_K;
+  const float* clip_V;
+  int32_t num_kv_heads, sink, recent, ngroups, fold_rv, max_batch, batch, nodes;
+  uint32_t* tickets;        // [max_batch], zero between launches
+  uint32_t* err_flags;
+};
+
+struct VerifyParams {
+  const float* probs;       // [B][nodes][vocab]
+  const float* draft_probs; // [B][nodes][vocab] or null
+  const int32_t* tokens;    // [B][nodes]
+  const int32_t* parent;    // [B][nodes]
+  const int32_t* draft_len; // [B] or null
+  const float* u_accept;    // [B][nodes]
+  const float* u_sample;    // [B]
+  int32_t* path;            // [B][nodes]
+  int32_t* n_path;          // [B]
+  int32_t* next_token;      // [B]
+  int32_t batch, nodes, vocab;
+  int32_t ctas;             // CTAs (one cluster) per request, set by launch_verify_draft
+  uint32_t* err_flags;      // may be null
+};
+
+struct RopeParams {
+  const __nv_bfloat16* qkv; // [tokens] rows of (Hq + 2 Hkv) x 128, row_stride elements apart
+  int64_t row_stride, tokens;
+  const int32_t* pos;       // [tokens]
+  const unsigned long long* turns;   // [rotary / 2] turns per position, 64-bit fractions
+  const __nv_bfloat16* q_weight;     // [128], both null: no norm
+  const __nv_bfloat16* k_weight;
+  float eps;
+  int32_t rotary, interleaved, num_q_heads, num_kv_heads;
+  __nv_bfloat16* q;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+};
+
 // Programmatic dependent launch: kernels launched with launch_pdl may start
 // while the previous kernel on the stream is still running. Before its
 // pdl_wait a kernel touches only constant data (rotations, their images), reads
@@ -226,6 +309,10 @@ int prefill_image_bytes();
 cudaError_t launch_decode(const DecodeParams& p, int batch, cudaStream_t s, cudaEvent_t ev_before = nullptr,
                           cudaEvent_t ev_after = nullptr);
 int decode_smem_bytes();
+cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t s);
+cudaError_t launch_commit_draft(const CommitParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_verify_draft(const VerifyParams& p, cudaStream_t s);
+cudaError_t launch_qkv_norm_rope(const RopeParams& p, cudaStream_t s);
 // offline calibration: causal attention outputs of every query head into o_ws
 // (calib_workspace_bytes), then C_Q and C_S per KV head (fp32 [hkv][128][128])
 size_t calib_workspace_bytes(int n, int hq);

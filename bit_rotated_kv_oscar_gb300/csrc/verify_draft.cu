@@ -1,0 +1,317 @@
+// Verification of a tree of drafted tokens against the target's probabilities.
+//
+// p_i is the target's distribution after node i of the tree, x_i the token of node
+// i. From node 0 on, at node i with children c_1 < c_2 < ... and the given uniform
+// number u_i the next node of the accepted path is
+//   without draft probabilities: the first c_m with u_i < sum over the distinct
+//     tokens of c_1 .. c_m of p_i(x): a draw from p_i by inversion with the
+//     children's tokens laid first, so the path is distributed like the target;
+//   with them (q_i, the distribution that node i's only child was drawn from): the
+//     child if u_i q_i(x) < p_i(x).
+// At the last node the token after the path is drawn by inversion with another
+// uniform number w over the weights
+//   p_i, if the node has no child; p_i without the children's tokens; or
+//   max(p_i - q_i, 0): the first token whose running sum exceeds w times the total.
+//
+// Sums: probabilities are taken as 64-bit fixed point (2^-44), so the sums are
+// integers, exact whatever their order, and the same inputs give the same token
+// on any launch shape. One probability is off by at most 2^-45, far below fp32.
+//
+// Bound: HBM, the last node's row of p (and q) once: a cluster of CTAs shares a
+// request's row, each warp sums one contiguous piece, and only the warp that holds
+// the token reads its piece again (from L2).
+#include "oscar_internal.cuh"
+#include "warp_mma.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+typedef unsigned long long u64;
+
+// probability as 2^-44 fixed point: clamped to [0, 1], NaN is 0
+__device__ __forceinline__ u64 fix(float p) {
+  return __float2ull_rn(fminf(fmaxf(p, 0.f), 1.f) * 17592186044416.f);
+}
+__device__ __forceinline__ u64 shfl_u64(u64 x, int src) { return __shfl_sync(0xffffffffu, x, src); }
+__device__ __forceinline__ u64 warp_sum_u64(u64 x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ u64 peer_u64(const u64* local, int rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(local), r;
+  u64 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];\n" : "=l"(v) : "r"(r) : "memory");
+  return v;
+}
+
+// weights of 4 consecutive entries from `at` (a multiple of 4 away from the row's
+// 16-byte boundary when vec); entries outside [lo, hi) are 0
+__device__ __forceinline__ void load4(const float* row, int at, int lo, int hi, bool vec, float (&x)[4]) {
+  if (vec && at >= lo && at + 4 <= hi) {
+    const float4 v = *reinterpret_cast<const float4*>(row + at);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = at + e >= lo && at + e < hi ? row[at + e] : 0.f;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) oscar_verify_draft_kernel(VerifyParams p) {
+  const int C = p.ctas, rank = blockIdx.x % C, b = blockIdx.x / C;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.nodes, V = p.vocab;
+  __shared__ int s_par[kTreeNodes], s_tok[kTreeNodes];
+  __shared__ u64 s_mass[kTreeNodes];
+  __shared__ int s_node, s_ok;
+  __shared__ u64 s_kids, s_warp[kWarps], s_total;
+  pdl_wait();
+  pdl_trigger();
+  const int len = p.draft_len ? p.draft_len[b] : T;
+  if (warp == 0) {
+    bool ok = len >= 0 && len <= T;
+    float pt[2] = {0.f, 0.f};
+    bool good[2] = {false, false};
+    int par[2] = {-2, -2};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int i = lane + 32 * n;
+      if (ok && i < len) {
+        const int q = p.parent[(size_t)b * T + i];
+        const int t = i ? p.tokens[(size_t)b * T + i] : 0;   // node 0's own token takes no part
+        if ((i == 0 ? q == -1 : q >= 0 && q < i) && t >= 0 && t < V) {
+          par[n] = q;
+          s_tok[i] = t;
+          if (i) {
+            const size_t at = ((size_t)b * T + q) * V + t;
+            pt[n] = p.probs[at];
+            // exact in 64 bits: two 24-bit factors
+            if (p.draft_probs)
+              good[n] = (double)p.u_accept[(size_t)b * T + q] * (double)p.draft_probs[at] < (double)pt[n];
+          }
+        } else {
+          par[n] = -3;
+        }
+      }
+      s_par[i] = par[n];
+      s_mass[i] = fix(pt[n]);
+    }
+    ok = !__any_sync(0xffffffffu, !ok || par[0] == -3 || par[1] == -3);
+    __syncwarp();
+    if (ok) {
+      bool twice = false;   // a second child where the draft's probabilities allow only one
+      bool again[2] = {false, false};   // an earlier sibling's token: counted once
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int i = lane + 32 * n;
+        if (i < len)
+          for (int j = 1; j < i; ++j) {
+            twice |= s_par[j] == par[n];
+            again[n] |= s_par[j] == par[n] && s_tok[j] == s_tok[i];
+          }
+      }
+      __syncwarp();
+      if (again[0]) s_mass[lane] = 0;
+      if (again[1]) s_mass[lane + 32] = 0;
+      __syncwarp();
+      if (!p.draft_probs) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int i = lane + 32 * n;
+          if (i < 1 || i >= len || again[n]) continue;
+          u64 mass = 0;
+          for (int j = 1; j <= i; ++j) mass += s_par[j] == par[n] ? s_mass[j] : 0;
+          const float u = fminf(fmaxf(p.u_accept[(size_t)b * T + par[n]], 0.f), 1.f);   // NaN counts as 0
+          good[n] = mass > __float2ull_rd(u * 17592186044416.f);
+        }
+      }
+      if (p.draft_probs && __any_sync(0xffffffffu, twice)) ok = false;
+    }
+    int node = 0, steps = 0;
+    u64 kids = 0;   // the last node's children
+    if (ok && len > 0) {
+      int32_t* path = p.path + (size_t)b * T;
+      for (;;) {
+        if (rank == 0 && lane == 0) path[steps] = node;
+        ++steps;
+        const uint32_t k0 = __ballot_sync(0xffffffffu, par[0] == node), k1 = __ballot_sync(0xffffffffu, par[1] == node);
+        const uint32_t g0 = __ballot_sync(0xffffffffu, par[0] == node && good[0]);
+        const uint32_t g1 = __ballot_sync(0xffffffffu, par[1] == node && good[1]);
+        if (!(g0 | g1)) {
+          kids = (u64)k1 << 32 | k0;
+          break;
+        }
+        node = g0 ? __ffs(g0) - 1 : 31 + __ffs(g1);
+      }
+    }
+    if (rank == 0) {
+      for (int i = lane; i < T; i += 32)
+        if (i >= steps) p.path[(size_t)b * T + i] = -1;
+      if (lane == 0) {
+        p.n_path[b] = steps;
+        if (steps == 0) p.next_token[b] = -1;
+        if (!ok && p.err_flags) atomicOr(p.err_flags, OSCAR_FLAG_BAD_TREE);
+      }
+    }
+    if (lane == 0) {
+      s_node = node;
+      s_kids = kids;
+      s_ok = ok && len > 0;
+    }
+  }
+  __syncthreads();
+  if (!s_ok) return;   // the same in every CTA of the cluster
+  const int node = s_node;
+  const u64 kids = s_kids;
+  const float* row = p.probs + ((size_t)b * T + node) * V;
+  const float* qrow = p.draft_probs ? p.draft_probs + ((size_t)b * T + node) * V : nullptr;
+  const int skew = (int)((reinterpret_cast<uintptr_t>(row) >> 2) & 3);   // entries past a 16-byte boundary
+  const bool qvec = qrow && (int)((reinterpret_cast<uintptr_t>(qrow) >> 2) & 3) == skew;
+  // pieces of whole 128-entry steps, counted from the boundary before the row
+  const int steps = (V + skew + 127) / 128, per = (steps + C * kWarps - 1) / (C * kWarps);
+  const int w0 = (rank * kWarps + warp) * per * 128 - skew, w1 = min(w0 + per * 128, V);
+  for (bool mode = kids != 0; ; mode = false) {   // refused weights, then (if they are all 0) the node's own
+    const bool less = mode && qrow, without = mode && !qrow;
+    auto weights = [&](int at, u64 (&f)[4]) {
+      float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+      load4(row, at, 0, w1, true, x);
+      if (less) load4(qrow, at, 0, w1, qvec, y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = fix(x[e]);
+        if (less) {
+          const u64 q = fix(y[e]);
+          f[e] = f[e] > q ? f[e] - q : 0;
+        }
+      }
+    };
+    u64 sum = 0;
+#pragma unroll 4
+    for (int at = w0 + 4 * lane; at < w1; at += 128) {
+      u64 f[4];
+      weights(at, f);
+      sum += (f[0] + f[1]) + (f[2] + f[3]);
+    }
+    sum = warp_sum_u64(sum);
+    if (without) {   // the children's tokens take no part (a repeated token's mass is 0 here)
+      u64 out = 0;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int i = lane + 32 * n;
+        if (((kids >> i) & 1) && s_tok[i] >= w0 && s_tok[i] < w1) out += s_mass[i];
+      }
+      sum -= warp_sum_u64(out);
+    }
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      u64 t = 0;
+      for (int w = 0; w < kWarps; ++w) t += s_warp[w];
+      s_total = t;
+    }
+    cluster_sync();
+    u64 total = 0, before = 0;
+    for (int r = 0; r < C; ++r) {
+      const u64 t = peer_u64(&s_total, r);
+      if (r < rank) before += t;
+      total += t;
+    }
+    cluster_sync();   // no CTA leaves, or writes its total again, while a peer reads it
+    if (total == 0) {
+      if (mode) continue;
+      if (rank == 0 && tid == 0) {
+        p.next_token[b] = -1;
+        if (p.err_flags) atomicOr(p.err_flags, OSCAR_FLAG_BAD_TREE);
+      }
+      return;
+    }
+    // the first token whose running sum exceeds w total; the product is off by less
+    // than one unit, and a w of 1 or more takes the last token with any weight
+    const double w = (double)fminf(fmaxf(p.u_sample[b], 0.f), 1.f);
+    u64 goal = (u64)(w * (double)total);
+    if (goal >= total) goal = total - 1;
+    for (int i = 0; i < warp; ++i) before += s_warp[i];
+    if (goal < before || goal >= before + s_warp[warp]) return;
+    for (int base = w0; base < w1; base += 128) {
+      const int at = base + 4 * lane;
+      u64 f[4] = {0, 0, 0, 0};
+      if (at < w1) weights(at, f);
+      if (without)
+        for (u64 k = kids; k; k &= k - 1) {
+          const int out = s_tok[__ffsll((long long)k) - 1] - at;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e == out) f[e] = 0;
+        }
+      u64 run = (f[0] + f[1]) + (f[2] + f[3]);
+      const u64 own = run;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 up = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + run > goal);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          u64 acc = before + run - own;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool was = acc > goal;
+            acc += f[e];
+            if (!was && acc > goal) p.next_token[b] = at + e;
+          }
+        }
+        return;
+      }
+      before += shfl_u64(run, 31);
+    }
+    return;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_verify_draft(const VerifyParams& p, cudaStream_t s) {
+  static PerDeviceOnce attrs;
+  static PerDeviceValue sm_count;
+  const cudaError_t ea = once_for_current_device(attrs, [] {
+    return cudaFuncSetAttribute(oscar_verify_draft_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (ea != cudaSuccess) return ea;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int num_sms = sm_count.get(dev, [dev] {
+    int n = 0;
+    return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0 ? n : 1;
+  });
+  // about four CTAs per SM in all, at least 2048 entries each, at most 16 to a cluster
+  int c = 1;
+  while (c < 16 && (int64_t)2 * c * p.batch <= 4 * num_sms && p.vocab / (2 * c) >= 2048) c *= 2;
+  VerifyParams q = p;
+  q.ctas = c;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.batch * c));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)c;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, oscar_verify_draft_kernel, q);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace oscar

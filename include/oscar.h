@@ -105,6 +105,7 @@ typedef enum oscar_status {
 #define OSCAR_FLAG_BAD_PAGE_ID 1u   /* a page-table entry outside [0, num_pages); access skipped */
 #define OSCAR_FLAG_BAD_STATE 2u     /* a sequence state breaking the invariants; request skipped */
 #define OSCAR_FLAG_TIMEOUT 4u       /* a bounded wait inside a kernel expired; its remaining work skipped */
+#define OSCAR_FLAG_BAD_TREE 8u      /* a draft length, parent, path or token outside its range; request skipped */
 
 typedef struct oscar_config {
   int32_t num_q_heads;
@@ -270,6 +271,115 @@ int oscar_decode_step_host(oscar_ctx* ctx, const int32_t* page_table, oscar_seq_
 
 /* Number of INT2 splits per (request, KV head) decode uses for `batch`. */
 int oscar_decode_splits(const oscar_ctx* ctx, int32_t batch, int32_t* splits);
+
+/* Drafted tokens (speculative decoding). The pages describe one token per step;
+ * these calls add the target model's side of verifying several at once. A
+ * request's draft is a tree of n_draft <= OSCAR_MAX_DRAFT nodes: node 0 is the
+ * last token sampled, whose key and value are not cached yet, and every other
+ * node i hangs on parent[i] < i. draft_len (DEVICE int32 [batch], or NULL for
+ * n_draft everywhere) is how many of the nodes a request uses, 0 .. n_draft;
+ * rows of the others are neither read nor written. One step is
+ *   oscar_qkv_norm_rope   q, k, v of the nodes, per layer;
+ *   oscar_tree_attn       per layer;
+ *   oscar_verify_draft    once, from the target's probabilities;
+ *   oscar_commit_draft    per layer, the accepted path into the cache;
+ * all on the stream, without a host synchronisation.
+ */
+#define OSCAR_MAX_DRAFT 64
+
+/* Attention of a tree of drafted tokens: node i attends over all L cached
+ * positions of its request and over its ancestors and itself,
+ *   o_i = softmax(q_i K^T * softmax_scale) V.
+ * q: DEVICE bf16 [batch][n_draft][num_q_heads][128]; k, v: DEVICE bf16
+ * [batch][n_draft][num_kv_heads][128], the nodes' own keys and values (with
+ * fold_rv, values in the R_V basis); parent: DEVICE int32 [batch][n_draft],
+ * parent[b][0] = -1 and 0 <= parent[b][i] < i; o: DEVICE bf16, like q. The cache
+ * and the state are read, not changed. A request whose parents or draft_len
+ * break this sets OSCAR_FLAG_BAD_TREE, one with a bad state
+ * OSCAR_FLAG_BAD_STATE; its n_draft rows of o are set to zero.
+ * workspace: caller-owned DEVICE memory of oscar_tree_attn_workspace_bytes()
+ * bytes, which calls that may overlap on the GPU must not share (the query is 0
+ * for a bad argument). q, k, v, o and workspace 16-byte aligned.
+ * Statuses as for oscar_decode_attn; OSCAR_ERR_UNSUPPORTED for n_draft above
+ * OSCAR_MAX_DRAFT, OSCAR_ERR_OUT_OF_RANGE for a small workspace,
+ * OSCAR_ERR_INVALID_ARG for a misaligned pointer or when the current device is
+ * not the context's. */
+size_t oscar_tree_attn_workspace_bytes(const oscar_ctx* ctx, int32_t batch, int32_t n_draft);
+int oscar_tree_attn(oscar_ctx* ctx, const void* q, const void* k, const void* v, const int32_t* parent,
+                    const int32_t* draft_len, const int32_t* page_table, const oscar_seq_state* state, void* o,
+                    int32_t batch, int32_t n_draft, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Accepted rows of a draft into the cache: request b appends rows
+ * path[b][0 .. n_path[b] - 1] of k and v, in order. The same cache contents and
+ * state, byte for byte, as oscar_quant_append of the gathered rows (n_new =
+ * n_path[b] for request b alone), with the counts read on the device.
+ * k, v: DEVICE bf16 [batch][n_draft][num_kv_heads][128], 16-byte aligned, the
+ * layout oscar_tree_attn takes; path: DEVICE int32 [batch][n_draft]; n_path:
+ * DEVICE int32 [batch], 0 .. n_draft, as oscar_verify_draft writes them;
+ * page_table and state as for oscar_quant_append: page_table must map every
+ * position below the new int2_end. A request with a count or row index out of
+ * range sets OSCAR_FLAG_BAD_TREE and keeps its cache and state. Statuses as for
+ * oscar_tree_attn. */
+int oscar_commit_draft(oscar_ctx* ctx, const int32_t* page_table, oscar_seq_state* state, const void* k,
+                       const void* v, const int32_t* path, const int32_t* n_path, int32_t batch, int32_t n_draft,
+                       void* stream);
+
+/* Which drafted tokens the target accepts, and the token after them. No context.
+ * probs: DEVICE float32 [batch][n_draft][vocab], row i the target's distribution
+ * after node i, values in [0, 1] (others are clamped, NaN counts as 0);
+ * tokens: DEVICE int32 [batch][n_draft], node i's token (node 0's is not read);
+ * u_accept: DEVICE float32 [batch][n_draft] and u_sample: DEVICE float32 [batch],
+ * uniform numbers in [0, 1). From node 0 on, at node i with children c_1 < c_2 ..:
+ *  - draft_probs NULL: the path goes to the first c_m with u_accept[i] < the sum of
+ *    probs[i][x] over the distinct tokens x of c_1 .. c_m (a draw from probs[i]
+ *    with the children's tokens laid first, so the result is distributed like the
+ *    target's own sampling whatever the tree);
+ *  - draft_probs DEVICE float32 [batch][n_draft][vocab], row i the distribution
+ *    node i's child was drawn from; each node has at most one child: the path
+ *    goes to it if u_accept[i] * draft_probs[i][x] < probs[i][x].
+ * next_token is drawn at the path's last node i with u_sample, by inversion in
+ * token order: the first token whose running sum of weights exceeds u_sample times
+ * their total. Weights: probs[i] if node i has no child; else probs[i] without the
+ * children's tokens, or max(probs[i] - draft_probs[i], 0). If those are all 0,
+ * probs[i]; if that is too, next_token is -1 and OSCAR_FLAG_BAD_TREE is set. The
+ * sums are taken in units of 2^-44, exactly, so results do not depend on how the
+ * work is spread.
+ * path: DEVICE int32 [batch][n_draft], the accepted nodes from node 0 on, then -1;
+ * n_path: DEVICE int32 [batch], their number; next_token: DEVICE int32 [batch].
+ * draft_len 0 gives n_path 0 and next_token -1; so does a request with a parent,
+ * token or draft_len out of range, or a second child where draft_probs allows
+ * one, and OSCAR_FLAG_BAD_TREE is set in *err_flags (DEVICE uint32, or NULL).
+ * OSCAR_ERR_INVALID_ARG for a null pointer or a size below 1,
+ * OSCAR_ERR_UNSUPPORTED for n_draft > OSCAR_MAX_DRAFT or vocab > 262144,
+ * OSCAR_ERR_OUT_OF_RANGE for batch > 1048576, OSCAR_ERR_CUDA for a failed launch. */
+int oscar_verify_draft(const float* probs, const float* draft_probs, const int32_t* tokens, const int32_t* parent,
+                       const int32_t* draft_len, const float* u_accept, const float* u_sample, int32_t batch,
+                       int32_t n_draft, int32_t vocab, int32_t* path, int32_t* n_path, int32_t* next_token,
+                       uint32_t* err_flags, void* stream);
+
+/* q, k and v of a layer from its fused projection: split, per-head root-mean-square
+ * norm of q and k, position rotation. No context.
+ * qkv: DEVICE bf16, n_tokens rows of num_q_heads query, num_kv_heads key and
+ * num_kv_heads value heads of 128 channels, rows row_stride elements apart (a
+ * multiple of 8, at least the row's width). A query or key head x becomes
+ *   y = x w / sqrt(mean(x^2) + eps)   (w: q_weight or k_weight, DEVICE bf16 [128];
+ *                                      both NULL: y = x),
+ * then pairs (a, c) of its first rotary_dim channels, (i, i + rotary_dim / 2) or
+ * with interleaved (2 i, 2 i + 1), become (a cos - c sin, c cos + a sin) of the
+ * angle pos[t] * inv_freq[i]; the other channels stay y. fp32 throughout, rounded
+ * once. pos: DEVICE int32 [n_tokens], any sign. turns: DEVICE uint64
+ * [rotary_dim / 2] as oscar_rope_turns makes them (HOST: inv_freq / 2 pi as 64-bit
+ * fractions of a turn, so that angles of far positions keep their precision).
+ * q: DEVICE bf16 [n_tokens][num_q_heads][128], k, v: [n_tokens][num_kv_heads][128],
+ * dense: what oscar_quant_append, oscar_decode_step and oscar_tree_attn take. They
+ * must not overlap qkv. qkv, q, k, v and the weights 16-byte aligned.
+ * OSCAR_ERR_UNSUPPORTED for a rotary_dim that is not a multiple of 16 in 16 .. 128;
+ * OSCAR_ERR_INVALID_ARG, OSCAR_ERR_CUDA as usual. n_tokens 0 does nothing. */
+int oscar_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+int oscar_qkv_norm_rope(const void* qkv, int64_t row_stride, const int32_t* pos, const uint64_t* turns,
+                        int32_t rotary_dim, int32_t interleaved, const void* q_weight, const void* k_weight, float eps,
+                        void* q, void* k, void* v, int32_t n_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        void* stream);
 
 /* Read (and optionally clear) the device error flags. Synchronises the
  * device. flags receives an OR of OSCAR_FLAG_* bits. */
