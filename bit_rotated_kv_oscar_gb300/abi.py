@@ -180,27 +180,44 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _arg(name, t, dtype, shape):
-    """Device pointer of a tensor argument, checked: CUDA, dtype, shape, dense row-major."""
-    if t is None:
-        return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
-    if not t.is_cuda:
-        raise ValueError("%s: expected a CUDA tensor" % name)
-    return _ptr(t)
+class _Args:
+    """Tensor arguments of one call, checked: CUDA, one device, dtype, shape, dense row-major.
+    Each method returns what ctypes takes for the argument; `device` is their device's index."""
 
+    __slots__ = ("device",)
 
-def _on_device(*tensors):
-    """Context manager making the tensors' device current; they must share one."""
-    import torch
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError("tensors on different devices: %s" % sorted(map(str, devs)))
-    dev = devs.pop()
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors, got %s" % dev)
-    return torch.cuda.device(dev)
+    def __init__(self):
+        self.device = -2   # none seen yet (a host tensor has -1)
+
+    def __call__(self, name, t, dtype=None, shape=None):
+        if t is None:
+            return None
+        if dtype is not None and (t.dtype is not dtype or t.shape != shape):
+            raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous tensor (got strides %s)" % (name, tuple(t.stride())))
+        return self.pointer(name, t)
+
+    def pointer(self, name, t):
+        d = t.get_device()
+        if d != self.device:
+            if d < 0:
+                raise ValueError("%s: expected a CUDA tensor" % name)
+            if self.device != -2:
+                raise ValueError("%s: on device %d, the other tensors on device %d" % (name, d, self.device))
+            self.device = d
+        return t.data_ptr()
+
+    def call(self, fn, args, stream):
+        """fn(*args, stream) with the arguments' device current: on `stream`, or on that device's
+        current stream."""
+        import torch
+        d = self.device
+        raw = torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+        if torch.cuda.current_device() == d:
+            return fn(*args, raw)
+        with torch.cuda.device(d):
+            return fn(*args, raw)
 
 
 def _event(ev):
@@ -227,15 +244,13 @@ def verify_draft(probs, tokens, parent, u_accept, u_sample, path, n_path, next_t
     if probs.dim() != 3:
         raise ValueError("probs: expected [batch, n_draft, vocab], got %s" % list(probs.shape))
     b, t, v = probs.shape
-    with _on_device(probs, tokens, parent, u_accept, u_sample, path, n_path, next_token, draft_probs, draft_len,
-                    err_flags):
-        _check(lib().oscar_verify_draft(
-            _arg("probs", probs, f32, (b, t, v)), _arg("draft_probs", draft_probs, f32, (b, t, v)),
-            _arg("tokens", tokens, i32, (b, t)), _arg("parent", parent, i32, (b, t)),
-            _arg("draft_len", draft_len, i32, (b,)), _arg("u_accept", u_accept, f32, (b, t)),
-            _arg("u_sample", u_sample, f32, (b,)), b, t, v, _arg("path", path, i32, (b, t)),
-            _arg("n_path", n_path, i32, (b,)), _arg("next_token", next_token, i32, (b,)), _ptr(err_flags),
-            _stream(stream)))
+    arg, bt, b1 = _Args(), (b, t), (b,)
+    args = (arg("probs", probs, f32, (b, t, v)), arg("draft_probs", draft_probs, f32, (b, t, v)),
+            arg("tokens", tokens, i32, bt), arg("parent", parent, i32, bt), arg("draft_len", draft_len, i32, b1),
+            arg("u_accept", u_accept, f32, bt), arg("u_sample", u_sample, f32, b1), b, t, v,
+            arg("path", path, i32, bt), arg("n_path", n_path, i32, b1), arg("next_token", next_token, i32, b1),
+            arg("err_flags", err_flags))
+    _check(arg.call(lib().oscar_verify_draft, args, stream))
 
 
 def rope_turns(inv_freq):
@@ -257,18 +272,18 @@ def qkv_norm_rope(qkv, pos, turns, q, k, v, q_weight=None, k_weight=None, eps=1e
     bf = torch.bfloat16
     n, hq, hkv = q.shape[0], q.shape[1], k.shape[1]
     width = (hq + 2 * hkv) * 128
-    if qkv.dtype != bf or tuple(qkv.shape) != (n, width) or qkv.stride(1) != 1 or (n > 1 and qkv.stride(0) < width):
+    row, col = qkv.stride()
+    if qkv.dtype is not bf or qkv.shape != (n, width) or col != 1 or (n > 1 and row < width):
         raise ValueError("qkv: expected bf16 rows [%d, %d] with dense columns, got %s %s, strides %s"
-                         % (n, width, qkv.dtype, list(qkv.shape), tuple(qkv.stride())))
+                         % (n, width, qkv.dtype, list(qkv.shape), (row, col)))
     if turns.dim() != 1:
         raise ValueError("turns: expected [rotary_dim / 2]")
-    with _on_device(qkv, pos, turns, q, k, v, q_weight, k_weight):
-        _check(lib().oscar_qkv_norm_rope(
-            ctypes.c_void_p(qkv.data_ptr()), qkv.stride(0) if n > 1 else width,
-            _arg("pos", pos, torch.int32, (n,)), _arg("turns", turns, torch.int64, turns.shape), 2 * turns.shape[0],
-            1 if interleaved else 0, _arg("q_weight", q_weight, bf, (128,)), _arg("k_weight", k_weight, bf, (128,)),
-            eps, _arg("q", q, bf, (n, hq, 128)), _arg("k", k, bf, (n, hkv, 128)), _arg("v", v, bf, (n, hkv, 128)),
-            n, hq, hkv, _stream(stream)))
+    half, arg = turns.shape[0], _Args()
+    args = (arg.pointer("qkv", qkv), row if n > 1 else width, arg("pos", pos, torch.int32, (n,)),
+            arg("turns", turns, torch.int64, (half,)), 2 * half, 1 if interleaved else 0,
+            arg("q_weight", q_weight, bf, (128,)), arg("k_weight", k_weight, bf, (128,)), eps,
+            arg("q", q, bf, (n, hq, 128)), arg("k", k, bf, (n, hkv, 128)), arg("v", v, bf, (n, hkv, 128)), n, hq, hkv)
+    _check(arg.call(lib().oscar_qkv_norm_rope, args, stream))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -370,27 +385,24 @@ class Context:
         `parent`) over the cache and their own ancestors. workspace: a uint8 CUDA tensor of at
         least tree_attn_workspace_bytes(batch, n_draft) bytes."""
         import torch
-        c, bf = self.cfg, torch.bfloat16
-        with _on_device(q, k, v, parent, page_table, state, o, workspace, draft_len):
-            _check(lib().oscar_tree_attn(
-                self.handle, _arg("q", q, bf, (batch, n_draft, c.num_q_heads, 128)),
-                _arg("k", k, bf, (batch, n_draft, c.num_kv_heads, 128)),
-                _arg("v", v, bf, (batch, n_draft, c.num_kv_heads, 128)),
-                _arg("parent", parent, torch.int32, (batch, n_draft)),
-                _arg("draft_len", draft_len, torch.int32, (batch,)), _ptr(page_table), _ptr(state),
-                _arg("o", o, bf, (batch, n_draft, c.num_q_heads, 128)), batch, n_draft, _ptr(workspace),
-                workspace.numel() * workspace.element_size(), _stream(stream)), self.handle)
+        c, bf, i32, arg = self.cfg, torch.bfloat16, torch.int32, _Args()
+        rows, kv = (batch, n_draft, c.num_q_heads, 128), (batch, n_draft, c.num_kv_heads, 128)
+        args = (self.handle, arg("q", q, bf, rows), arg("k", k, bf, kv), arg("v", v, bf, kv),
+                arg("parent", parent, i32, (batch, n_draft)), arg("draft_len", draft_len, i32, (batch,)),
+                arg("page_table", page_table), arg("state", state), arg("o", o, bf, rows), batch, n_draft,
+                arg("workspace", workspace), workspace.numel() * workspace.element_size())
+        _check(arg.call(lib().oscar_tree_attn, args, stream), self.handle)
 
     def commit_draft(self, page_table, state, k, v, path, n_path, batch, n_draft, stream=None):
         """oscar_commit_draft: request b appends rows path[b, :n_path[b]] of k and v [batch, n_draft,
         Hkv, 128] to the cache."""
         import torch
-        c, bf, i32 = self.cfg, torch.bfloat16, torch.int32
-        with _on_device(page_table, state, k, v, path, n_path):
-            _check(lib().oscar_commit_draft(
-                self.handle, _ptr(page_table), _ptr(state), _arg("k", k, bf, (batch, n_draft, c.num_kv_heads, 128)),
-                _arg("v", v, bf, (batch, n_draft, c.num_kv_heads, 128)), _arg("path", path, i32, (batch, n_draft)),
-                _arg("n_path", n_path, i32, (batch,)), batch, n_draft, _stream(stream)), self.handle)
+        c, bf, i32, arg = self.cfg, torch.bfloat16, torch.int32, _Args()
+        kv = (batch, n_draft, c.num_kv_heads, 128)
+        args = (self.handle, arg("page_table", page_table), arg("state", state), arg("k", k, bf, kv),
+                arg("v", v, bf, kv), arg("path", path, i32, (batch, n_draft)), arg("n_path", n_path, i32, (batch,)),
+                batch, n_draft)
+        _check(arg.call(lib().oscar_commit_draft, args, stream), self.handle)
 
     def decode_splits(self, batch):
         s = ctypes.c_int32()
