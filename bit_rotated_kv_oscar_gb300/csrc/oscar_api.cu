@@ -12,6 +12,10 @@
 #include <vector>
 
 #include "oscar_internal.cuh"
+#include "tree_attn.cuh"
+#ifndef OSCAR_TREE_WARP_ROWS
+#define OSCAR_TREE_WARP_ROWS 32
+#endif
 
 using namespace oscar;
 
@@ -595,16 +599,17 @@ int oscar_decode_step_host(oscar_ctx* ctx, const int32_t* page_table, oscar_seq_
 
 // Launch shapes of a tree-attention call, the same for the workspace query and the call.
 struct TreePlan {
-  int rows, tile_rows, col_tiles, row_tiles, win_slots, splits;
+  int rows, tile_rows, col_tiles, row_tiles, images128, win_slots, splits;
   size_t rec_bytes, part_bytes;
 };
 static TreePlan tree_plan(const oscar_ctx* ctx, int batch, int nodes) {
   TreePlan t{};
   const int hkv = ctx->cfg.num_kv_heads;
   t.rows = nodes * (ctx->cfg.num_q_heads / hkv);
-  t.tile_rows = t.rows <= 16 ? 16 : 32;
+  t.tile_rows = t.rows <= 16 ? 16 : (t.rows <= OSCAR_TREE_WARP_ROWS ? 32 : 2 * kWideRows);
   t.col_tiles = (t.rows + t.tile_rows - 1) / t.tile_rows;
   t.row_tiles = (t.rows + 31) / 32;
+  t.images128 = (t.rows + kWideRows - 1) / kWideRows;
   t.win_slots = (ctx->cfg.sink + ctx->cfg.recent + nodes + kTreeWindowChunk - 1) / kTreeWindowChunk;
   // one wave of CTAs together with the BF16 ones, at most kSplitPages pages per CTA
   const int64_t units = (int64_t)batch * hkv * t.col_tiles, pages = ctx->cfg.max_pages_per_seq;
@@ -613,7 +618,8 @@ static TreePlan tree_plan(const oscar_ctx* ctx, int batch, int nodes) {
   s = std::min<int64_t>(s, (pages + 7) / 8);   // >= 8 pages per split: one per warp
   if (ctx->cfg.num_splits > 0) s = ctx->cfg.num_splits;
   t.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 256));
-  t.rec_bytes = ((size_t)batch * hkv * t.row_tiles * kTreeRecWords * 4 + 255) / 256 * 256;
+  const size_t rec = t.tile_rows == 2 * kWideRows ? (size_t)t.images128 * kWideRecBytes : (size_t)t.row_tiles * kTreeRecWords * 4;
+  t.rec_bytes = ((size_t)batch * hkv * rec + 255) / 256 * 256;
   t.part_bytes = (size_t)batch * hkv * (t.win_slots + t.splits) * t.rows * kPartFloats * sizeof(float);
   return t;
 }
@@ -674,6 +680,8 @@ int oscar_tree_attn(oscar_ctx* ctx, const void* q, const void* k, const void* v,
   p.images = ctx->images;
   p.rv16 = ctx->rv16;
   p.pv_scale = ctx->pv_scale;
+  p.clip_K = ctx->clip_K;
+  p.clip_V = ctx->clip_V;
   p.qrec = static_cast<uint32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + t.rec_bytes);
   p.o = static_cast<__nv_bfloat16*>(o);
@@ -690,6 +698,7 @@ int oscar_tree_attn(oscar_ctx* ctx, const void* q, const void* k, const void* v,
   p.tile_rows = t.tile_rows;
   p.col_tiles = t.col_tiles;
   p.row_tiles = t.row_tiles;
+  p.images128 = t.images128;
   p.win_slots = t.win_slots;
   p.splits = t.splits;
   p.scale_log2 = ctx->cfg.softmax_scale * 1.4426950408889634f;

@@ -183,13 +183,16 @@ struct TreeParams {
   const uint8_t* images;    // [Hkv][4][32 KiB]: R_K hi, R_K lo, ... (bf16, swizzled)
   const __half* rv16;       // [Hkv][128][128] R_V, row-major
   const float* pv_scale;    // [Hkv]
-  uint32_t* qrec;           // [B][Hkv][row_tiles][kTreeRecWords]
+  const float* clip_K;      // [Hkv]
+  const float* clip_V;
+  uint32_t* qrec;           // [B][Hkv][row_tiles][kTreeRecWords], or the wide kernel's images
   float* part;              // [B][Hkv][win_slots + splits][nodes * gqa][kPartFloats]
   __nv_bfloat16* o;         // [B][nodes][Hq][128]
   int32_t num_q_heads, num_kv_heads, gqa, sink, recent, ngroups, fold_rv, max_batch, batch, nodes;
-  int32_t tile_rows;        // query rows per attention CTA: 16 or 32
+  int32_t tile_rows;        // query rows per attention CTA: 16 or 32 (warp tiles), or 256
   int32_t col_tiles;        // tiles of tile_rows rows
-  int32_t row_tiles;        // records of 32 rows
+  int32_t row_tiles;        // tiles of 32 rows
+  int32_t images128;        // query images of 128 rows per (request, KV head) (wide kernel)
   int32_t win_slots, splits;
   float scale_log2;
   uint32_t* err_flags;

@@ -22,6 +22,7 @@
 //      of sink, ring and tree; one partial row (sum, maximum, denominator) each.
 //   3. oscar_tree_merge_kernel   log-sum-exp merge, R_V^T, normalisation, bf16.
 #include "int2_page.cuh"
+#include "tree_attn.cuh"
 #include "warp_mma.cuh"
 
 namespace oscar {
@@ -50,6 +51,8 @@ constexpr int kRotThreads = 128;
 constexpr int kImage = kHeadDim * kHeadDim * 2;   // bytes of one bf16 image
 constexpr int kRotSmem = 2 * kImage + 32 * kRow * 2;
 
+// WIDE: the record is the wide kernel's image (tree_attn.cuh)
+template <bool WIDE>
 __global__ void __launch_bounds__(kRotThreads) oscar_tree_rotate_kernel(TreeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -138,9 +141,33 @@ __global__ void __launch_bounds__(kRotThreads) oscar_tree_rotate_kernel(TreePara
         *reinterpret_cast<uint32_t*>(hs + (16 * mt + 8 * half + gid) * kRow + c) = f2_to_h2_bits(x0 * f, x1 * f);
       }
       sum = quad_sum(sum);
-      if (tig == 0) gsum[16 * mt + 8 * half + gid][warp] = sum * gscale;
+      if (tig == 0) gsum[16 * mt + 8 * half + gid][warp] = sum * (WIDE ? s2k * 0x1p-9f : gscale);   // 2^-9: far below fp16's end
     }
   __syncthreads();
+  if constexpr (WIDE) {
+    uint8_t* img = reinterpret_cast<uint8_t*>(p.qrec) +
+                   (((size_t)b * p.num_kv_heads + h) * p.images128 + (tile >> 2)) * kWideRecBytes;
+    const int r0 = 32 * (tile & 3);
+    for (int i = tid; i < 32 * 16; i += kRotThreads) {
+      const int r = i >> 4, u = i & 15;
+      *reinterpret_cast<uint4*>(img + sw128_off(r0 + r, u)) = *reinterpret_cast<const uint4*>(hs + r * kRow + 8 * u);
+    }
+    if (tid < 32) {   // hi and lo parts of the group sums, then zeros
+      const int ng = p.ngroups;
+      uint32_t w[8] = {};
+      for (int gq = 0; gq < ng; ++gq) {
+        const float v = ng == kGroups ? gsum[tid][gq] : gsum[tid][2 * gq] + gsum[tid][2 * gq + 1];
+        const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+        w[gq >> 1] |= (uint32_t)__half_as_ushort(hi) << (16 * (gq & 1));
+        w[(ng + gq) >> 1] |= (uint32_t)__half_as_ushort(lo) << (16 * (gq & 1));
+      }
+      uint8_t* x = img + kWideImage;
+      *reinterpret_cast<uint4*>(x + extra_off(r0 + tid, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(x + extra_off(r0 + tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (tid == 0) reinterpret_cast<float*>(img + kWideUnits)[tile & 3] = ldexpf(1.f, -k);
+    return;
+  }
   uint32_t* rec = p.qrec + (((size_t)b * p.num_kv_heads + h) * p.row_tiles + tile) * kTreeRecWords;
   for (int i = tid; i < 2 * 8 * 32; i += kRotThreads) {
     const int l = i & 31, kb = (i >> 5) & 7, mt = i >> 8;
@@ -347,7 +374,7 @@ __device__ __forceinline__ void page_values(const uint8_t* sb, int lane, const u
 template <int NG, int MT>
 __device__ void int2_part(const TreeParams& p, int b, int h, int tile, int split, int nsplits, int lo, int hi,
                           uint8_t* smem, uint4* qs, State<MT>& st, float& unit, float& inv_ps) {
-  constexpr int NP = MT == 1 ? 2 : 1;   // pages per softmax step
+  constexpr int NP = 1;   // pages per softmax step
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int first = lo / kPage;
   const int npages = hi > lo ? (hi - 1) / kPage - first + 1 : 0;
@@ -463,33 +490,6 @@ __device__ void int2_part(const TreeParams& p, int b, int h, int tile, int split
   }
   cp_wait<0>();
   if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
-}
-
-// ancestors (and self) of every node as bit masks, by pointer jumping
-__device__ void ancestor_masks(const int32_t* parent, int len, unsigned long long* anc, int* jump, int lane) {
-  for (int i = lane; i < kTreeNodes; i += 32) {
-    anc[i] = 1ull << i;
-    const int q = i < len ? parent[i] : -1;
-    jump[i] = q < i ? q : -1;
-  }
-  __syncwarp();
-  for (int r = 0; r < 6; ++r) {   // 2^6 = kTreeNodes steps up
-    unsigned long long a[2];
-    int q[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int i = lane + 32 * n, up = jump[i];
-      a[n] = up >= 0 ? anc[i] | anc[up] : anc[i];
-      q[n] = up >= 0 ? jump[up] : -1;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      anc[lane + 32 * n] = a[n];
-      jump[lane + 32 * n] = q[n];
-    }
-    __syncwarp();
-  }
 }
 
 constexpr int kBfChunk = kTreeWindowChunk;   // tokens per BF16 CTA: one 16-token tile for each warp
@@ -885,17 +885,21 @@ cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t s) {
     cudaError_t e = set_attrs<kGroups>();
     if (e == cudaSuccess) e = set_attrs<2>();
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(oscar_tree_rotate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRotSmem);
+      e = cudaFuncSetAttribute(oscar_tree_rotate_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRotSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(oscar_tree_rotate_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRotSmem);
     return e;
   });
   if (ea != cudaSuccess) return ea;
   static_assert(kRecUnit < kTreeRecWords, "query record");
   const int nslots = p.win_slots + p.splits, rows = p.nodes * p.gqa;
-  cudaError_t e = launch_pdl(oscar_tree_rotate_kernel, dim3(p.row_tiles, p.num_kv_heads, p.batch), dim3(kRotThreads),
+  const bool wide = p.tile_rows == 2 * kWideRows;
+  cudaError_t e = launch_pdl(wide ? oscar_tree_rotate_kernel<true> : oscar_tree_rotate_kernel<false>, dim3(p.row_tiles, p.num_kv_heads, p.batch), dim3(kRotThreads),
                              kRotSmem, s, p);
   const dim3 grid(p.col_tiles * nslots, p.num_kv_heads, p.batch);
   const bool one = p.tile_rows == 16;
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && wide) e = launch_tree_wide(p, s);
+  if (e == cudaSuccess && !wide)
     e = p.ngroups == kGroups
             ? launch_pdl(one ? oscar_tree_attn_kernel<kGroups, 1> : oscar_tree_attn_kernel<kGroups, 2>, grid,
                          dim3(kThreads), tree_smem(one ? 1 : 2), s, p)

@@ -1,0 +1,57 @@
+// Shared by the two attention kernels of drafted-token trees (tree_attn.cu and
+// tree_attn_wide.cu): the query image of the wide kernel and the tree's masks.
+#pragma once
+
+#include "oscar_internal.cuh"
+
+namespace oscar {
+
+// Query image of 128 rows for the wide kernel: q~ in fp16 as a K-major operand in
+// 128-byte-swizzle atoms of 64 channels (two of 16 KiB), then 16 more reduction
+// columns (4 KiB, 8-row x 16-byte core matrices, column halves 2 KiB apart): the fp16
+// hi parts of the NG group sums of q~, their lo parts, zeros; then one score unit for
+// each 32 rows.
+constexpr int kWideRows = 128;
+constexpr int kWideImage = 2 * 16384;
+constexpr int kWideExtra = 4096;
+constexpr int kWideUnits = kWideImage + kWideExtra;
+constexpr int kWideRecBytes = kWideUnits + 64;
+__host__ __device__ constexpr int sw128_off(int row, int chunk) {   // 16-byte chunk 0 .. 15 of a 128-channel row
+  return (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+__host__ __device__ constexpr int extra_off(int row, int chunk) { return chunk * 2048 + (row >> 3) * 128 + (row & 7) * 16; }
+
+// The power of two that brings a head's scales to the top of fp16 whatever its clip:
+// s <= 2 clip / 3 keeps s * 2^m finite.
+__device__ __forceinline__ int scale_exponent(float clip) { return max(0, min(15, (int)floorf(log2f(65504.f * 1.49f / clip)))); }
+
+// ancestors (and self) of every node as bit masks, by pointer jumping; one warp
+__device__ inline void ancestor_masks(const int32_t* parent, int len, unsigned long long* anc, int* jump, int lane) {
+  for (int i = lane; i < kTreeNodes; i += 32) {
+    anc[i] = 1ull << i;
+    const int q = i < len ? parent[i] : -1;
+    jump[i] = q < i ? q : -1;
+  }
+  __syncwarp();
+  for (int r = 0; r < 6; ++r) {   // 2^6 = kTreeNodes steps up
+    unsigned long long a[2];
+    int q[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int i = lane + 32 * n, up = jump[i];
+      a[n] = up >= 0 ? anc[i] | anc[up] : anc[i];
+      q[n] = up >= 0 ? jump[up] : -1;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      anc[lane + 32 * n] = a[n];
+      jump[lane + 32 * n] = q[n];
+    }
+    __syncwarp();
+  }
+}
+
+cudaError_t launch_tree_wide(const TreeParams& p, cudaStream_t s);
+
+}  // namespace oscar

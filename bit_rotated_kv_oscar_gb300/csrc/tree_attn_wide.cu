@@ -1,0 +1,895 @@
+// Attention of a tree of drafted tokens: the 5th-generation tensor-core kernel, for
+// more query rows per KV head than one warp tile holds (see tree_attn.cu for the
+// operator, its rotation and merge).
+//
+// A CTA per SM takes up to 256 query rows (nodes x query heads of one KV head) and a
+// slice of the pages, 128 tokens (8 pages) at a time. Its warps have three roles, tied by
+// mbarriers:
+//   8 warps dequantise, one page each: K^ = s c as [token][channel] and V^ = s c + z as
+//     [channel][token], fp16, into two stages of swizzled shared memory. The block layout
+//     gives lane (a, b) the code words of tokens a, a + 8 and channels 2 b, 2 b + 1
+//     (mod 8), whose fp16 pairs land in 32 different banks for every store. Raw pages
+//     arrive by cp.async.
+//   2 warps, one per softmax group, issue the products: S = Q~ K^T, 128 x 128 x 144, and O += P V^, 128 x 128 x
+//     128, P in tensor memory. The 16 further reduction columns of S are the keys' zero
+//     points against the group sums of q~ (hi and lo parts), so only q~ and 3 s are
+//     rounded.
+//   2 groups of 4 softmax warps, thread = row: P = 2^(S - max) in fp16 over S. With more
+//     than 128 rows each group has its own row tile; otherwise both share the rows and
+//     take alternate token tiles, each with its own O, maximum and sum, merged at the end.
+//
+// A code in slot i of a word reads as c * 4^i * 2^-24 (int2_page.cuh); 4^i is divided out
+// of q~ for the scores and of O's channel blocks for the values.
+//
+// The BF16 part (sink, ring and the tree's own nodes) is the same computation in the raw
+// basis on bf16 operands; its probabilities are split into two bf16 parts.
+//
+// What bounds it: see the figures at the launcher.
+#include "int2_page.cuh"
+#include "tc_ptx.cuh"
+#include "tree_attn.cuh"
+#include "warp_mma.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kSoftWarps = 8, kDeqWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kDeqWarps;   // and the next: one issuing warp per group
+constexpr int kThreads = 32 * (kMmaWarp + 2);
+constexpr int kTile = 128;              // tokens
+constexpr uint32_t kTmem = 512;         // group g: S (or P) in columns 128 g .., O in 256 + 128 g ..
+constexpr float kLazyMost = 256.f;      // the running maximum moves when a probability exceeds this
+constexpr int kRawStages = 3;           // page copies in flight per dequantising warp, with one row tile
+constexpr int kAhead = 8;                // token tiles whose pages are brought into L2 ahead of their copy
+constexpr int kRawBytes = kDeqWarps * kBlockBytes;
+
+struct Shared {
+  uint8_t k[2][kWideImage];
+  uint8_t v[2][kWideImage];             // [channel][token]
+  uint8_t kx[2][kWideExtra];
+  uint8_t q[kWideImage + kWideExtra];   // q~ (or raw q) of the first row tile
+  uint8_t q2[kWideImage + kWideExtra];  // of the second; with one row tile, raw pages
+  uint8_t raw[kRawBytes];               // raw pages with two row tiles
+  float ml[kSoftWarps][32][2];
+  unsigned long long anc[kTreeNodes];
+  int jump[kTreeNodes];
+  uint64_t kfull[2], kfree[2], vfull[2], vfree[2];   // per stage
+  uint64_t sfull[2][2], pfull[2][2], ofull[2], done;   // per group and half of the tile, per group
+  uint32_t tmem;
+  int abort;
+  uint16_t valid[4][8];                 // [tile % 4][page] bit t: token t takes part
+};
+static_assert(kRawStages * kRawBytes <= kWideImage + kWideExtra, "raw pages in the second query image");
+
+constexpr uint32_t idesc(bool bf16, uint32_t n) {   // fp32 accumulators, K-major operands, M = 128
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// The products are issued by one lane of a warp whose lanes all follow the same path
+// (`lead` is set in one of them): their operands then stay in uniform registers.
+// both operands in shared memory
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+// the row operand in tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
+}
+// K-major operand without swizzle: 8-row x 16-byte core matrices, the two along the
+// reduction 2 KiB apart, row groups 128 bytes apart
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | (uint64_t)(2048 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\ntcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+// the same load without its wait; tmem_ready16 ties the registers behind a later one
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ready16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
+  __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                      *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// two fp32 operations at once, each rounded like the scalar one
+__device__ __forceinline__ uint64_t pair_of(float f) { return (uint64_t)__float_as_uint(f) << 32 | __float_as_uint(f); }
+__device__ __forceinline__ void fma_pair(uint32_t x0, uint32_t x1, uint64_t b, uint64_t c, float& y0, float& y1) {
+  asm("{\n .reg .b64 t;\n mov.b64 t, {%2, %3};\n fma.rn.f32x2 t, t, %4, %5;\n mov.b64 {%0, %1}, t;\n}\n"
+      : "=f"(y0), "=f"(y1) : "r"(x0), "r"(x1), "l"(b), "l"(c));
+}
+__device__ __forceinline__ void add_pair(uint64_t& s, float x0, float x1) {
+  asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n add.rn.f32x2 %0, %0, t;\n}\n" : "+l"(s) : "f"(x0), "f"(x1));
+}
+__device__ __forceinline__ float sum_pairs(uint64_t a, uint64_t b) {
+  float x, y;
+  asm("{\n .reg .b64 t;\n add.rn.f32x2 t, %2, %3;\n mov.b64 {%0, %1}, t;\n}\n" : "=f"(x), "=f"(y) : "l"(a), "l"(b));
+  return x + y;
+}
+__device__ __forceinline__ uint32_t half2_of(float x) {
+  const __half2 r = __float2half2_rn(x);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bounded wait on an mbarrier phase: a poll every NS nanoseconds, for about a second.
+// Polling warps take issue slots from the working ones, hence the sleep and the short loop.
+template <int NS>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, %3;\n"
+      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " nanosleep.u32 %4;\n sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
+      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity & 1u), "n"(1000000000 / NS), "n"(NS)
+      : "memory");
+  return done != 0;
+}
+
+// bits of a token pair's two halves
+__device__ __forceinline__ uint32_t pair_mask(uint32_t valid, int t0, int t1) {
+  return (((valid >> t0) & 1u) ? 0x0000ffffu : 0u) | (((valid >> t1) & 1u) ? 0xffff0000u : 0u);
+}
+
+// a staged page in registers: this lane's code words and metadata (see include/oscar.h)
+template <int NG>
+struct Page {
+  uint4 k, v, vm[NG];
+  uint32_t ks[NG], kz[2];
+};
+template <int NG>
+__device__ __forceinline__ void read_page(Page<NG>& g, const uint8_t* raw, int lane) {
+  const int a = lane >> 2, b = lane & 3;
+  g.k = *reinterpret_cast<const uint4*>(raw + 16 * lane);
+  g.v = *reinterpret_cast<const uint4*>(raw + 512 + 16 * lane);
+#pragma unroll
+  for (int gq = 0; gq < NG; ++gq) {
+    g.ks[gq] = *reinterpret_cast<const uint32_t*>(raw + kscale_off(NG, a, gq));
+    g.vm[gq] = *reinterpret_cast<const uint4*>(raw + vscale_off(NG, 0, 0) + 16 * (4 * gq + b));
+  }
+  g.kz[0] = *reinterpret_cast<const uint32_t*>(raw + kzero_off(NG, lane & 15, 0));
+  g.kz[1] = NG == kGroups ? *reinterpret_cast<const uint32_t*>(raw + kzero_off(NG, lane & 15, NG - 2)) : 0u;
+}
+// tokens whose bit in `valid` is clear get scale and zero 0
+template <int NG>
+__device__ __forceinline__ void mask_page(Page<NG>& g, uint32_t valid, int lane) {
+  const int a = lane >> 2, b = lane & 3;
+  const uint32_t mk = pair_mask(valid, a, a + 8), m0 = pair_mask(valid, 2 * b, 2 * b + 1),
+                 m1 = pair_mask(valid, 2 * b + 8, 2 * b + 9);
+#pragma unroll
+  for (int gq = 0; gq < NG; ++gq) {
+    g.ks[gq] &= mk;
+    g.vm[gq].x &= m0;
+    g.vm[gq].y &= m1;
+    g.vm[gq].z &= m0;
+    g.vm[gq].w &= m1;
+  }
+  if (!((valid >> (lane & 15)) & 1u)) g.kz[0] = g.kz[1] = 0u;
+}
+
+// keys of page `pg` (0 .. 7) of its tile: s c 4^i 2^(m - 24) at rows 16 pg + (a, a + 8)
+template <int NG>
+__device__ __forceinline__ void store_keys(const Page<NG>& g, uint32_t sk, uint32_t skx, int pg, int lane, uint32_t mul,
+                                           uint32_t zmul) {
+  const int a = lane >> 2, b = lane & 3;
+  const uint4 w = g.k, wh = shr10(w);
+  uint32_t s0[NG], s1[NG];   // scales of tokens a and a + 8, in both halves
+#pragma unroll
+  for (int gq = 0; gq < NG; ++gq) {
+    const uint32_t s = wm::hmul2_bits(g.ks[gq], mul);
+    s0[gq] = __byte_perm(s, s, 0x1010);
+    s1[gq] = __byte_perm(s, s, 0x3232);
+  }
+  const uint32_t base = sk + (uint32_t)((16 * pg + a) * 128 + (a << 4) + 4 * b);
+#define OSCAR_K(I)                                                                                     \
+  {                                                                                                    \
+    constexpr int gq = (I) / (8 / NG), at = ((I) >> 2) * 16384, c0 = 2 * ((I) & 3) * 16, c1 = c0 + 16; \
+    sts32((base ^ c0) + at, wm::hmul2_bits(slot_bits<I>(w.x, wh.x), s0[gq]));                          \
+    sts32((base ^ c1) + at, wm::hmul2_bits(slot_bits<I>(w.y, wh.y), s0[gq]));                          \
+    sts32((base ^ c0) + at + 1024, wm::hmul2_bits(slot_bits<I>(w.z, wh.z), s1[gq]));                   \
+    sts32((base ^ c1) + at + 1024, wm::hmul2_bits(slot_bits<I>(w.w, wh.w), s1[gq]));                   \
+  }
+  OSCAR_K(0) OSCAR_K(1) OSCAR_K(2) OSCAR_K(3) OSCAR_K(4) OSCAR_K(5) OSCAR_K(6) OSCAR_K(7)
+#undef OSCAR_K
+  if (lane < 16) {
+    const uint32_t z0 = wm::hmul2_bits(g.kz[0], zmul), z1 = wm::hmul2_bits(g.kz[1], zmul);
+    const uint32_t at = skx + extra_off(16 * pg + lane, 0);
+    if constexpr (NG == kGroups)
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%1,%2};\n" ::"r"(at), "r"(z0), "r"(z1) : "memory");
+    else
+      asm volatile("st.shared.v4.b32 [%0], {%1,%1,%2,%2};\n" ::"r"(at), "r"(z0), "r"(0u) : "memory");
+  }
+}
+
+// its values: (s c 4^i + z 4^i) 2^(m - 24) of token pairs at channel rows 16 i + 8 x + a
+template <int NG>
+__device__ __forceinline__ void store_values(const uint4& w, const uint4 (&vm)[NG], uint32_t sv, int pg, int lane,
+                                             uint32_t mul, uint32_t zmul) {
+  const int a = lane >> 2, b = lane & 3;
+  const uint4 wh = shr10(w);
+  const uint32_t row = sv + (uint32_t)((pg >> 2) * 16384 + a * 128 + 4 * b);
+  const uint32_t b0 = row + (uint32_t)(((2 * (pg & 3)) ^ a) << 4), b1 = row + (uint32_t)(((2 * (pg & 3) + 1) ^ a) << 4);
+  uint32_t s0[NG], s1[NG], z0[NG], z1[NG];
+#pragma unroll
+  for (int gq = 0; gq < NG; ++gq) {
+    s0[gq] = wm::hmul2_bits(vm[gq].x, mul);
+    s1[gq] = wm::hmul2_bits(vm[gq].y, mul);
+    z0[gq] = wm::hmul2_bits(vm[gq].z, zmul);
+    z1[gq] = wm::hmul2_bits(vm[gq].w, zmul);
+  }
+#define OSCAR_V(I)                                                                         \
+  {                                                                                        \
+    constexpr int gq = (I) / (8 / NG), at = 2048 * (I);                                    \
+    constexpr int e = 6 + 2 * ((I) <= 4 ? (I) : (I) - 5);   /* 4^i 2^-9 as fp16 bits */    \
+    constexpr uint32_t f = (uint32_t)(e << 10) * 0x10001u;                                 \
+    const uint32_t y0 = wm::hmul2_bits(z0[gq], f), y1 = wm::hmul2_bits(z1[gq], f);         \
+    sts32(b0 + at, hfma2_bits(slot_bits<I>(w.x, wh.x), s0[gq], y0));                       \
+    sts32(b0 + at + 1024, hfma2_bits(slot_bits<I>(w.y, wh.y), s0[gq], y0));                \
+    sts32(b1 + at, hfma2_bits(slot_bits<I>(w.z, wh.z), s1[gq], y1));                       \
+    sts32(b1 + at + 1024, hfma2_bits(slot_bits<I>(w.w, wh.w), s1[gq], y1));                \
+  }
+  OSCAR_V(0) OSCAR_V(1) OSCAR_V(2) OSCAR_V(3) OSCAR_V(4) OSCAR_V(5) OSCAR_V(6) OSCAR_V(7)
+#undef OSCAR_V
+}
+
+__device__ __forceinline__ void apply_mask(uint32_t (&s)[16], uint32_t mask) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (!((mask >> j) & 1u)) s[j] = 0xff800000u;   // -inf
+}
+
+// what every role knows of the CTA's work
+struct Work {
+  bool int2;
+  int pbeg, pend, lo, hi;       // INT2 pages and positions
+  int t0, nwin, ns, nr, rb;     // BF16 window tokens t0 .. t0 + nwin - 1
+  int ntiles, nrt, njobs;       // token tiles, row tiles, softmax jobs
+  int rep;                      // copies of the rows in the row tile: 4 up to 32 rows, 2 up to 64
+  int row0, nrow, len, row;     // query rows, nodes used, window row
+  // job j is done by group j % 2, on token tile:
+  __device__ __forceinline__ int tile_of(int j) const { return nrt == 2 ? j >> 1 : j; }
+};
+
+// dequantising warp w: page w of every token tile
+template <int NG>
+__device__ void dequantise(const TreeParams& p, Shared& sm, const Work& wk, int b, int h, int w, int lane) {
+  volatile int* abort = &sm.abort;
+  constexpr int kBB = block_bytes(NG);
+  const int32_t* table = p.page_table + (size_t)b * p.pt_stride;
+  const uint8_t* pool_h = p.pool + (size_t)h * kBB + 16 * lane;
+  const size_t stride = (size_t)p.num_kv_heads * kBB;
+  const int stages = wk.nrt == 2 ? 1 : kRawStages;
+  uint8_t* ring = (wk.nrt == 2 ? sm.raw : sm.q2) + w * stages * kBlockBytes;
+  const uint32_t sring = smem_u32(ring) + 16 * lane;
+  const int mk = scale_exponent(p.clip_K[h]), mv = scale_exponent(p.clip_V[h]);
+  const uint32_t kmul = half2_of(ldexpf(1.f, mk)), kzmul = half2_of(ldexpf(1.f, mk - 15));
+  const uint32_t vmul = half2_of(ldexpf(1.f, mv)), vzmul = half2_of(ldexpf(1.f, mv - 15));
+  bool bad = false;
+  // this warp's page ids of tiles 32 n .. 32 n + 31, one per lane
+  auto load_ids = [&](int t) {
+    const int at = wk.pbeg + 8 * (t + lane) + w;
+    int id = -1;
+    if (at < wk.pend) {
+      id = at < p.pt_stride ? table[at] : -1;
+      if (id < 0 || id >= p.num_pages) {
+        bad = true;
+        id = -1;
+      }
+    }
+    return id;
+  };
+  // page ids of tiles 32 n .. + 31 and of the next 32 (one per lane); the pages of tile
+  // t + kAhead are brought into L2 while tile t's copy is issued
+  int ids = load_ids(0), next = load_ids(32);
+  uint32_t okbits = 0u;   // bit t % 32: tile t's page has a valid id
+  auto prefetch = [&](int t, int t0) {   // page of tile t, whose ids are relative to tile t0
+    const int id = __shfl_sync(0xffffffffu, t - t0 < 32 ? ids : next, t & 31);
+    if (id >= 0 && lane < (kBB + 127) / 128)
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(pool_h + (size_t)id * stride + 112 * lane));
+  };
+  int base = 0;   // first tile of `ids`
+  auto issue = [&](int t, int slot) {
+    if (t < wk.ntiles) {
+      if (t == base + 32) {
+        base = t;
+        ids = next;
+        next = load_ids(t + 32);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, t & 31);
+      okbits = (okbits & ~(1u << (t & 31))) | ((uint32_t)(id >= 0) << (t & 31));
+      const uint32_t nb = id >= 0 ? 16u : 0u, dst = sring + slot * kBlockBytes;
+      const uint8_t* src = pool_h + (size_t)max(id, 0) * stride;
+      wm::cp_async16(dst, src, nb);
+      wm::cp_async16(dst + 512, src + 512, nb);
+      if (NG == kGroups || lane < 16) wm::cp_async16(dst + 1024, src + 1024, nb);
+      prefetch(t + kAhead, base);
+    }
+    wm::cp_commit();
+  };
+  for (int t = 0; t < kAhead; ++t) prefetch(t, 0);
+  for (int t = 0; t < stages; ++t) issue(t, t);
+  // step t stores the values of tile t and the keys of tile t + 1
+  int slot = 0;
+  Page<NG> pg;
+  uint4 vcode = make_uint4(0u, 0u, 0u, 0u), vmeta[NG];
+  for (int t = -1; t < wk.ntiles; ++t) {
+    const int n = t + 1, sn = n & 1, st = t & 1;
+    const bool more = n < wk.ntiles;
+    if (t >= 0) {
+      vcode = pg.v;
+#pragma unroll
+      for (int gq = 0; gq < NG; ++gq) vmeta[gq] = pg.vm[gq];
+    }
+    if (more) {
+      if (stages == 1) wm::cp_wait<0>();
+      else wm::cp_wait<kRawStages - 1>();
+      __syncwarp();
+      read_page<NG>(pg, ring + slot * kBlockBytes, lane);
+      const uint32_t valid = page_token_bits((okbits >> (n & 31)) & 1u, (wk.pbeg + 8 * n + w) * kPage, wk.lo, wk.hi);
+      __syncwarp();   // the page is in registers: its slot is refilled
+      issue(n + stages, slot);
+      slot = slot + 1 == stages ? 0 : slot + 1;
+      if (valid != 0xffffu) mask_page<NG>(pg, valid, lane);
+      if (lane == 0) sm.valid[n & 3][w] = (uint16_t)valid;
+    }
+    const bool ok = !*abort && (!more || n < 2 || wait_phase<100>(&sm.kfree[sn], (uint32_t)((n >> 1) - 1))) &&
+                    (t < 2 || wait_phase<100>(&sm.vfree[st], (uint32_t)((t >> 1) - 1)));
+    if (!__all_sync(0xffffffffu, ok)) {   // given up: the other roles stop before their next wait
+      *abort = 1;
+      break;
+    }
+    if (more) store_keys<NG>(pg, smem_u32(sm.k[sn]), smem_u32(sm.kx[sn]), w, lane, kmul, kzmul);
+    if (t >= 0) store_values<NG>(vcode, vmeta, smem_u32(sm.v[st]), w, lane, vmul, vzmul);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (more) mbar_arrive(smem_u32(&sm.kfull[sn]));
+      if (t >= 0) mbar_arrive(smem_u32(&sm.vfull[st]));
+    }
+  }
+  wm::cp_wait<0>();
+  if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
+}
+
+// the BF16 tile: keys as they are, values transposed to [channel][token]; i of n threads
+__device__ void window_tile(const TreeParams& p, Shared& sm, const Work& wk, int b, int h, int i0, int n) {
+  const size_t slots = (size_t)(p.sink + p.recent);
+  const __nv_bfloat16* win = p.window + ((size_t)wk.row * p.num_kv_heads + h) * 2 * slots * kHeadDim;
+  auto row_of = [&](int t, int kind) -> const __nv_bfloat16* {   // window token t0 + t
+    const int w = wk.t0 + t;
+    if (w < wk.ns + wk.nr) return win + (kind * slots + (w < wk.ns ? w : p.sink + (wk.rb + w - wk.ns) % p.recent)) * kHeadDim;
+    return (kind ? p.v : p.k) + (((size_t)b * p.nodes + (w - wk.ns - wk.nr)) * p.num_kv_heads + h) * kHeadDim;
+  };
+  const uint32_t sk = smem_u32(sm.k[0]), sv = smem_u32(sm.v[0]);
+  for (int i = i0; i < kTile * 16; i += n) {
+    const int t = i >> 4, u = i & 15;
+    wm::cp_async16(sk + sw128_off(t, u), t < wk.nwin ? row_of(t, 0) + 8 * u : win, t < wk.nwin ? 16u : 0u);
+  }
+  wm::cp_commit();
+  for (int i = i0; i < 64 * 16; i += n) {   // token pair, 8 channels
+    const int t = 2 * (i & 63), u = i >> 6;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (t < wk.nwin) x = *reinterpret_cast<const uint4*>(row_of(t, 1) + 8 * u);
+    if (t + 1 < wk.nwin) y = *reinterpret_cast<const uint4*>(row_of(t + 1, 1) + 8 * u);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      sts32(sv + sw128_off(8 * u + e, t >> 3) + 2 * (t & 7), __byte_perm(xs[e >> 1], ys[e >> 1], (e & 1) ? 0x7632 : 0x5410));
+  }
+  wm::cp_wait<0>();
+}
+
+// the issuing warp of group g: its jobs g, g + 2, ..., each in two halves of 64 tokens, so
+// that one half's products run while the softmax works on the other. Descriptors are
+// prepared once, a step along an operand adds a constant to the low word.
+__device__ void issue_products(Shared& sm, const Work& wk, uint32_t tmem, int g, uint32_t lead) {
+  volatile int* abort = &sm.abort;
+  const uint32_t id = idesc(!wk.int2, 128), id_s = idesc(!wk.int2, 64);
+  const uint8_t* qs = wk.nrt == 2 && g ? sm.q2 : sm.q;
+  const uint64_t dq = sw128_desc(smem_u32(qs)), dqx = plain_desc(smem_u32(qs) + kWideImage);
+  const uint64_t dk = sw128_desc(smem_u32(sm.k[0])), dv = sw128_desc(smem_u32(sm.v[0])), dx = plain_desc(smem_u32(sm.kx[0]));
+  const uint32_t s = tmem + 128 * g, o = s + 256;
+  auto wait = [&](uint64_t* bar, int n) {
+    return __all_sync(0xffffffffu, !*abort && wait_phase<20>(bar, (uint32_t)n)) != 0;
+  };
+  auto scores = [&](int j, int half) {
+    const int t = wk.tile_of(j), st = t & 1;
+    if (half == 0) {
+      if (!wait(&sm.kfull[st], t >> 1)) return false;
+      tc_fence_after();
+    }
+    // tokens 64 half ..: 64 rows of 128 bytes further in each atom
+    const uint64_t k = dk + (uint32_t)st * (kWideImage >> 4) + (uint32_t)half * (8192 >> 4);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+      umma_ss(s + 64 * half, dq + off, k + off, id_s, kk ? 1u : 0u, lead);
+    }
+    if (wk.int2)
+      umma_ss(s + 64 * half, dqx, dx + (uint32_t)st * (kWideExtra >> 4) + (uint32_t)half * (1024 >> 4), id_s, 1u, lead);
+    commit_lead(&sm.sfull[g][half], lead);
+    if (half) commit_lead(&sm.kfree[st], lead);
+    return true;
+  };
+  bool ok = g >= wk.njobs || (scores(g, 0) && scores(g, 1));
+  for (int j = g; ok && j < wk.njobs; j += 2) {
+    const int t = wk.tile_of(j), st = t & 1;
+    for (int half = 0; ok && half < 2; ++half) {
+      ok = (half || wait(&sm.vfull[st], t >> 1)) && wait(&sm.pfull[g][half], j >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t v = dv + (uint32_t)st * (kWideImage >> 4) + (uint32_t)half * (16384 >> 4);
+      const uint32_t at = s + 64 * half;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t a = at + 32 * (kk >> 1) + 8 * (kk & 1);
+        const uint64_t bd = v + (uint32_t)((kk * 32) >> 4);
+        if (!wk.int2) umma_ts(o, a + 16, bd, id, half || kk ? 1u : 0u, lead);   // the low parts
+        umma_ts(o, a, bd, id, !wk.int2 || j > 1 || half || kk ? 1u : 0u, lead);
+      }
+      commit_lead(&sm.ofull[g], lead);
+      if (half) commit_lead(&sm.vfree[st], lead);
+      // its S is overwritten only now: one warp's products run in issue order
+      if (j + 2 < wk.njobs) ok = scores(j + 2, half);
+    }
+  }
+  if (!ok) *abort = 1;
+  commit_lead(&sm.done, lead);
+}
+
+// scales this row's O (with_o) and the P of 16-token blocks c0 .. c1 - 1 of the row: a new
+// maximum was met
+__device__ __noinline__ void rescale_rows(uint32_t ts, uint32_t to, int c0, int c1, bool int2, bool with_o, float a) {
+  if (with_o) {
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      uint32_t o[16];
+      tmem_ld16(to + 16 * c, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+      tmem_st16(to + 16 * c, o);
+    }
+  }
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+#pragma unroll 1
+    for (int part = 0; part < (int2 ? 1 : 2); ++part) {
+      const uint32_t at = ts + 32 * (c >> 1) + 8 * (c & 1) + 16 * part;
+      uint32_t x[8];
+      tmem_ld8(at, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (int2) {
+          const float2 f = wm::h2_bits_to_f2(x[i]);
+          x[i] = wm::f2_to_h2_bits(f.x * a, f.y * a);
+        } else {
+          const float2 f = wm::bf2_bits_to_f2(x[i]);
+          x[i] = wm::f2_to_bf2_bits(f.x * a, f.y * a);
+        }
+      }
+      tmem_st8(at, x);
+    }
+  }
+}
+
+// softmax of one half of a job: N blocks of 32 tokens from block c0 on (ts: the row's S).
+// One pass over the scores: the probabilities of 32 tokens are taken against the running
+// maximum and kept in registers; only if one of them exceeds kLazyMost (or the maximum is
+// unset) is the maximum moved, O and the P written so far rescaled and the 32 taken again.
+// pv: value products issued before (each half job's is one phase of ofull).
+template <int N, bool INT2>
+__device__ __forceinline__ void softmax_half(Shared& sm, uint32_t ts, uint32_t to, const uint32_t (&mask)[2], bool masked, int c0,
+                                             int g, int pv, float unit, float& m, float& l) {
+  const uint32_t t0 = ts + 32 * c0;
+  uint32_t x[2][16];
+  tmem_ld16_async(t0, x[0]);
+  tmem_ld16_async(t0 + 16, x[1]);
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    float e[32];
+    float nb = m == -INFINITY ? 0.f : -m * unit, top;
+    auto probabilities = [&]() {
+      tmem_wait_ld();
+      tmem_ready16(x[0]);
+      tmem_ready16(x[1]);
+      if (masked) {
+        apply_mask(x[0], mask[c]);
+        apply_mask(x[1], mask[c] >> 16);
+      }
+      float t4[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t uu = pair_of(unit), nn = pair_of(nb);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float a0, a1;
+        fma_pair(x[i >> 4][i & 15], x[i >> 4][(i & 15) + 1], uu, nn, a0, a1);
+        e[i] = wm::ex2(a0);
+        e[i + 1] = wm::ex2(a1);
+        t4[(i >> 1) & 3] = fmaxf(t4[(i >> 1) & 3], fmaxf(e[i], e[i + 1]));
+      }
+      top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+    };
+    probabilities();
+    const bool over = top > kLazyMost || m == -INFINITY;
+    if (__any_sync(0xffffffffu, over)) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i >> 4][i & 15]));
+      const bool bump = over && mx > m;
+      const float a = bump ? wm::ex2((m - mx) * unit) : 1.f;
+      if (pv) wait_phase<20>(&sm.ofull[g], (uint32_t)(pv - 1));   // a wait that runs out shows at the next one, too
+      tc_fence_after();
+      if (__any_sync(0xffffffffu, bump && (c || pv))) rescale_rows(ts, to, 2 * c0, 2 * (c0 + c), INT2, pv != 0, a);
+      m = bump ? mx : m;
+      l *= a;
+      nb = m == -INFINITY ? 0.f : -m * unit;   // no token so far: every score is -inf
+      probabilities();
+    }
+    if (c + 1 < N) {
+      tmem_ld16_async(t0 + 32 * (c + 1), x[0]);
+      tmem_ld16_async(t0 + 32 * (c + 1) + 16, x[1]);
+    }
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) add_pair(sum[(i >> 1) & 1], e[i], e[i + 1]);
+    l += sum_pairs(sum[0], sum[1]);
+    // P of the 32 tokens takes the place of their scores
+    uint32_t y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)   // fp16: off by at most 2^-11 of it; the denominator sums the fp32 ones
+      y[i] = INT2 ? wm::f2_to_h2_bits(e[2 * i], e[2 * i + 1]) : wm::f2_to_bf2_bits(e[2 * i], e[2 * i + 1]);
+    tmem_st16(t0 + 32 * c, y);
+    if (!INT2) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = wm::bf2_bits_to_f2(y[i]);
+        y[i] = wm::f2_to_bf2_bits(e[2 * i] - f.x, e[2 * i + 1] - f.y);
+      }
+      tmem_st16(t0 + 32 * c + 16, y);
+    }
+  }
+}
+
+// softmax warp `warp` of group g: thread = row, jobs g, g + 2, ... With few rows the row
+// tile holds copies of them (Work::rep) and each copy takes its own tokens; the others'
+// probabilities are 0 in its rows.
+template <bool INT2>
+__device__ void softmax_rows(const TreeParams& p, Shared& sm, const Work& wk, uint32_t tmem, int g, int warp, int lane,
+                             float unit, float& m, float& l) {
+  volatile int* abort = &sm.abort;
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16, ts = tmem + lanes + 128 * g, to = ts + 256;
+  const int blocks = 4 / wk.rep;   // warps that hold different rows
+  const int row = (wk.nrt == 2 ? kWideRows * g : 0) + 32 * (warp % blocks);
+  const bool active = row < wk.nrow;
+  const int first = warp / blocks * blocks;   // this copy's 32-token blocks: first .. first + blocks - 1
+  m = -INFINITY;
+  l = 0.f;
+  unsigned long long sees = 0;
+  if (!INT2) sees = sm.anc[min((wk.row0 + row + lane) / p.gqa, kTreeNodes - 1)];
+  for (int j = g; j < wk.njobs; j += 2) {
+    for (int half = 0; half < 2; ++half) {
+      const bool ready = !*abort && wait_phase<40>(&sm.sfull[g][half], (uint32_t)(j >> 1));
+      if (!__all_sync(0xffffffffu, ready)) {
+        *abort = 1;
+        return;
+      }
+      tc_fence_after();
+      if (active) {
+        const int t = wk.tile_of(j), c0 = max(first, 2 * half), n = min(first + blocks, 2 * half + 2) - c0;
+        uint32_t mask[2] = {~0u, ~0u};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c >= n) break;
+          if (INT2) {
+            mask[c] = reinterpret_cast<const uint32_t*>(sm.valid[t & 3])[c0 + c];
+          } else {
+            // tokens 32 (c0 + c) .. + 31: cached ones, then the nodes this row descends from
+            const int d0 = wk.t0 + 32 * (c0 + c) - (wk.ns + wk.nr), left = wk.nwin - 32 * (c0 + c);
+            const unsigned long long s = d0 >= 64 ? 0ull : d0 >= 0 ? sees >> d0
+                                         : d0 <= -32 ? ~0ull : (sees << -d0) | ((1ull << -d0) - 1ull);
+            mask[c] = (uint32_t)s & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u);
+          }
+        }
+        const bool masked = !__all_sync(0xffffffffu, (mask[0] & mask[1]) == ~0u);
+        const int pv = j / 2 * 2 + half;
+        if (n == 2) softmax_half<2, INT2>(sm, ts, to, mask, masked, c0, g, pv, unit, m, l);
+        else if (n == 1) softmax_half<1, INT2>(sm, ts, to, mask, masked, c0, g, pv, unit, m, l);
+        if (n < 2) {
+          const uint32_t z[16] = {};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int at = 2 * half + c;
+            if (n <= 0 || at != c0) {
+              tmem_st16(ts + 32 * at, z);
+              if (!INT2) tmem_st16(ts + 32 * at + 16, z);
+            }
+          }
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[g][half]));
+    }
+  }
+}
+
+template <int NG>
+__global__ void __launch_bounds__(kThreads, 1) oscar_tree_wide_kernel(TreeParams p) {
+  extern __shared__ uint8_t raw_smem[];
+  Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = blockIdx.x % p.col_tiles, slot = blockIdx.x / p.col_tiles, h = blockIdx.y, b = blockIdx.z;
+  const int g = p.gqa, S = p.sink, W = p.recent;
+  pdl_wait();
+  pdl_trigger();
+  const oscar_seq_state seq = p.state[b];
+  const int len = p.draft_len ? p.draft_len[b] : p.nodes;
+  Work wk;
+  wk.row0 = tile * 2 * kWideRows;
+  wk.nrow = min(2 * kWideRows, len * g - wk.row0);
+  // a bad state or length: the merge writes the request's zeros and reads no partial
+  if (!state_ok(seq, S, W, p.max_batch) || len < 0 || len > p.nodes || wk.nrow <= 0) return;
+  const int nslots = p.win_slots + p.splits, rows = p.nodes * g;
+  float* part = p.part + ((((size_t)b * p.num_kv_heads + h) * nslots + slot) * rows + wk.row0) * (size_t)kPartFloats;
+  wk.len = len;
+  wk.row = seq.window_row;
+  wk.nrt = wk.nrow > kWideRows ? 2 : 1;
+  wk.rep = wk.nrow <= 32 ? 4 : wk.nrow <= 64 ? 2 : 1;
+  wk.int2 = slot >= p.win_slots;
+  const int L = seq.seq_len;
+  wk.lo = S;
+  wk.hi = min(seq.int2_end, L);
+  wk.ns = min(S, L);
+  wk.rb = max(seq.int2_end, S);
+  wk.nr = max(L - wk.rb, 0);
+  wk.pbeg = wk.pend = wk.t0 = wk.nwin = 0;
+  if (wk.int2) {
+    const int first = wk.lo / kPage, npages = wk.hi > wk.lo ? (wk.hi - 1) / kPage - first + 1 : 0;
+    const int chunk = ((npages + p.splits - 1) / p.splits + 7) / 8 * 8;   // whole tiles
+    wk.pbeg = first + (slot - p.win_slots) * chunk;
+    wk.pend = min(wk.pbeg + chunk, first + npages);
+    wk.ntiles = max((wk.pend - wk.pbeg + 7) / 8, 0);
+  } else {
+    wk.t0 = slot * kTile;
+    wk.nwin = min(kTile, wk.ns + wk.nr + len - wk.t0);
+    wk.ntiles = wk.nwin > 0 ? 1 : 0;
+  }
+  wk.njobs = wk.ntiles * wk.nrt;
+  if (wk.ntiles == 0) {   // no keys: the merge skips the slot
+    for (int i = tid; i < wk.nrow; i += kThreads) {
+      part[(size_t)i * kPartFloats + kHeadDim] = -INFINITY;
+      part[(size_t)i * kPartFloats + kHeadDim + 1] = 0.f;
+    }
+    return;
+  }
+
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(kTmem));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.kfull[i]), kDeqWarps);
+      mbar_init(smem_u32(&sm.kfree[i]), wk.nrt);   // a stage is read by every row tile
+      mbar_init(smem_u32(&sm.vfull[i]), kDeqWarps);
+      mbar_init(smem_u32(&sm.vfree[i]), wk.nrt);
+      for (int half = 0; half < 2; ++half) {
+        mbar_init(smem_u32(&sm.sfull[i][half]), 1);
+        mbar_init(smem_u32(&sm.pfull[i][half]), kSoftWarps / 2);
+      }
+      mbar_init(smem_u32(&sm.ofull[i]), 1);
+    }
+    mbar_init(smem_u32(&sm.done), 2);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  // query operands of the row tiles
+  const uint8_t* rec = nullptr;
+  if (wk.int2) {
+    rec = reinterpret_cast<const uint8_t*>(p.qrec) +
+          (((size_t)b * p.num_kv_heads + h) * p.images128 + 2 * tile) * (size_t)kWideRecBytes;
+    constexpr int n16 = (kWideImage + kWideExtra) / 16;
+    for (int i = tid; i < wk.nrt * n16; i += kThreads) {
+      const int r = i >= n16, u = i - r * n16;
+      // 16-byte piece u: rows lie 8 to an atom row of 64 (or, in the extra columns, 8)
+      // pieces, so a copy of the first 128 / rep rows repeats that many pieces
+      const int per = (u < kWideImage / 16 ? 1024 : 128) / wk.rep, src = wk.rep == 1 ? u : u - (u % (per * wk.rep)) / per * per;
+      wm::cp_async16(smem_u32(r ? sm.q2 : sm.q) + 16 * u, rec + (size_t)r * kWideRecBytes + 16 * src);
+    }
+    // reduction columns 8 .. 15 of the zero-point operand stay 0
+    for (int i = tid; i < 2 * kTile; i += kThreads)
+      asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(smem_u32(sm.kx[i >> 7]) + extra_off(i & 127, 1)), "r"(0u)
+                   : "memory");
+  } else {
+    for (int i = tid; i < wk.nrt * kWideRows * 16; i += kThreads) {
+      const int r = i >> 4, u = i & 15, rr = wk.nrt == 2 ? r : r % (kWideRows / wk.rep);
+      const int col = wk.row0 + rr, node = col / g, m = col - node * g;
+      const bool in = rr < wk.nrow;
+      const size_t off = in ? (((size_t)b * p.nodes + node) * p.num_q_heads + h * g + m) * kHeadDim + 8 * u : 0;
+      wm::cp_async16(smem_u32(r >= kWideRows ? sm.q2 : sm.q) + sw128_off(r & (kWideRows - 1), u), p.q + off, in ? 16u : 0u);
+    }
+    if (warp == 0) ancestor_masks(p.parent + (size_t)b * p.nodes, len, sm.anc, sm.jump, lane);
+  }
+  wm::cp_commit();
+  wm::cp_wait<0>();
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  float m = -INFINITY, l = 0.f, unit = p.scale_log2;
+  if (warp >= kMmaWarp) {
+    issue_products(sm, wk, tmem, warp - kMmaWarp, lane == 0);
+  } else if (warp >= kSoftWarps) {
+    const int w = warp - kSoftWarps;
+    if (wk.int2) {
+      dequantise<NG>(p, sm, wk, b, h, w, lane);
+    } else {
+      window_tile(p, sm, wk, b, h, tid - 32 * kSoftWarps, 32 * kDeqWarps);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.kfull[0]));
+        mbar_arrive(smem_u32(&sm.vfull[0]));
+      }
+    }
+  } else {
+    const int gr = warp >> 2, w = warp & 3;
+    if (wk.int2) {
+      const int mk = scale_exponent(p.clip_K[h]), rt = wk.nrt == 2 ? gr : 0, block = w % (4 / wk.rep);
+      const bool active = kWideRows * rt + 32 * block < wk.nrow;
+      unit = (active ? reinterpret_cast<const float*>(rec + (size_t)rt * kWideRecBytes + kWideUnits)[block] : 1.f) *
+             ldexpf(1.f, 24 - mk);
+    }
+    if (wk.int2) softmax_rows<true>(p, sm, wk, tmem, gr, w, lane, unit, m, l);
+    else softmax_rows<false>(p, sm, wk, tmem, gr, w, lane, unit, m, l);
+    sm.ml[warp][lane][0] = m * unit;   // log2 units
+    sm.ml[warp][lane][1] = l;
+  }
+  // every product has ended (or, after a wait that ran out, those that were issued)
+  const bool ended = wait_phase<100>(&sm.done, 0u);
+  const bool good = !__syncthreads_or(!ended || *(volatile int*)&sm.abort);
+  tc_fence_after();
+  if (!good) {
+    if (tid == 0) atomicOr(p.err_flags, OSCAR_FLAG_TIMEOUT);
+    for (int i = tid; i < wk.nrow; i += kThreads) {
+      part[(size_t)i * kPartFloats + kHeadDim] = -INFINITY;
+      part[(size_t)i * kPartFloats + kHeadDim + 1] = 0.f;
+    }
+  } else {
+    // every softmax warp's O, weighted, to shared memory (the operand stages are free),
+    // then the sums of the warps that hold the same rows: copies and, with one row tile,
+    // both groups
+    float* stage = reinterpret_cast<float*>(sm.k);   // [8 warps][32 rows][kStageRow]
+    constexpr int kStageRow = kHeadDim + 4;
+    static_assert(kSoftWarps * 32 * kStageRow * 4 <= 4 * kWideImage + 2 * kWideExtra, "O stage");
+    const int blocks = 4 / wk.rep;
+    if (warp < kSoftWarps) {
+      const int gr = warp >> 2, w = warp & 3;
+      const bool used = (wk.nrt == 2 ? kWideRows * gr : 0) + 32 * (w % blocks) < wk.nrow && gr < wk.njobs;
+      if (used) {
+        float M = -INFINITY;
+        for (int x = 0; x < kSoftWarps; ++x)
+          if (x % blocks == w % blocks && (wk.nrt == 1 || x >> 2 == gr)) M = fmaxf(M, sm.ml[x][lane][0]);
+        const float mine = sm.ml[warp][lane][0];
+        const float a = (mine == -INFINITY ? 0.f : wm::ex2(mine - M)) *
+                        (wk.int2 ? ldexpf(1.f, 24 - scale_exponent(p.clip_V[h])) : 1.f);
+        const uint32_t to = tmem + ((uint32_t)(32 * w) << 16) + 256 + 128 * gr;
+        float* dst = stage + (warp * 32 + lane) * kStageRow;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // channel block i carries its slot's factor
+          uint32_t o[16];
+          tmem_ld16(to + 16 * i, o);
+          const float f = wk.int2 ? a / slot_factor(i) : a;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float4*>(dst + 16 * i + 4 * e) =
+                make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f, __uint_as_float(o[4 * e + 2]) * f,
+                            __uint_as_float(o[4 * e + 3]) * f);
+        }
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    const int copies = wk.nrt == 2 ? 1 : wk.rep, groups = wk.nrt == 2 ? 1 : min(wk.njobs, 2);
+    for (int i = tid; i < wk.nrow * 32; i += kThreads) {
+      const int r = i >> 5, c = 4 * (i & 31), w0 = wk.nrt == 2 ? r >> 5 : (r >> 5) % blocks, ln = r & 31;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < copies * groups; ++x) {
+        const int w = w0 + (x % copies) * blocks + 4 * (x / copies);
+        const float4 y = *reinterpret_cast<const float4*>(stage + (w * 32 + ln) * kStageRow + c);
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
+      *reinterpret_cast<float4*>(part + (size_t)r * kPartFloats + c) = o;
+      if (c == 0) {
+        float M = -INFINITY, sum = 0.f;
+        for (int x = 0; x < copies * groups; ++x) M = fmaxf(M, sm.ml[w0 + (x % copies) * blocks + 4 * (x / copies)][ln][0]);
+        for (int x = 0; x < copies * groups; ++x) {
+          const float* ml = sm.ml[w0 + (x % copies) * blocks + 4 * (x / copies)][ln];
+          sum += ml[0] == -INFINITY ? 0.f : ml[1] * wm::ex2(ml[0] - M);
+        }
+        *reinterpret_cast<float2*>(part + (size_t)r * kPartFloats + kHeadDim) = make_float2(M, sum);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmem));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_wide(const TreeParams& p, cudaStream_t s) {
+  static PerDeviceOnce attrs;
+  constexpr int smem = (int)sizeof(Shared) + 1024;
+  const cudaError_t ea = once_for_current_device(attrs, [] {
+    cudaError_t e = cudaFuncSetAttribute(oscar_tree_wide_kernel<kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(oscar_tree_wide_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e;
+  });
+  if (ea != cudaSuccess) return ea;
+  const dim3 grid(p.col_tiles * (p.win_slots + p.splits), p.num_kv_heads, p.batch);
+  return launch_pdl(p.ngroups == kGroups ? oscar_tree_wide_kernel<kGroups> : oscar_tree_wide_kernel<2>, grid, dim3(kThreads),
+                    smem, s, p);
+}
+
+}  // namespace oscar

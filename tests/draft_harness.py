@@ -36,11 +36,13 @@ def tree_reference(cache, q, k, v, parent, n):
     worst case of the kernel's roundings before its bf16 output.
 
     The roundings (the fp32 sums add about 2^-20 of the same terms, covered by 2^-18): a
-    score s = sum_i q~_i k_i has q~ rounded to fp16, so |ds| <= 2^-11 sum |q~_i k_i|, and
-    scores off by at most D change a softmax average of v by at most (e^(2D) - 1) sum p |v|.
-    Probabilities are rounded before both sums, their products with the value scales once
-    more (2^-11 each way against sum p |v|, twice for the code and zero parts); the
-    un-rotation rounds its two operands to fp16 (2 * 2^-11 of sum_k |x_k| |R_ck|)."""
+    score s = sum_i q~_i k_i, k_i = s c + z, has q~ rounded to fp16 and (with many query
+    rows) the products s c as well, so |ds| <= 2^-11 sum |q~_i| (|k_i| + |s c|), and scores
+    off by at most D change a softmax average of v by at most (e^(2D) - 1) sum p |v|.
+    Probabilities are rounded once, their products with the value scales or the values
+    themselves once more, and a sum may be normalised by unrounded ones (3 * 2^-11 of
+    sum p |v|); the un-rotation rounds its two operands to fp16 (2 * 2^-11 of
+    sum_k |x_k| |R_ck|)."""
     hkv = cache.k.shape[1]
     g = q.shape[1] // hkv
     see = ancestors(parent, n)
@@ -49,7 +51,10 @@ def tree_reference(cache, q, k, v, parent, n):
     lo, hi = cache.int2_lo, cache.int2_hi
     for h in range(hkv):
         kh, vh = cache.raw_kv(h)
-        kr = np.abs(kh[lo:hi] @ cache.r_k[h])       # the INT2 keys as the kernel sees them
+        if hi > lo:   # the INT2 keys as the kernel sees them
+            zero = np.repeat(cache.k_zero[:, h].astype(np.float64), cache.group, axis=-1)
+            kr = kh[lo:hi] @ cache.r_k[h]
+            kr = np.abs(kr) + np.abs(kr - zero)
         vr = vh[lo:hi] @ cache.r_v[h]
         kk = np.concatenate([kh, k[:n, h]])
         vv = np.concatenate([vh, v[:n, h]])
