@@ -28,13 +28,26 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxVocab = 1 << 18;
+constexpr int kMaxSteps = (kMaxVocab + 3 + 127) / 128 / kWarps + 1;   // 128-entry steps of a warp's piece
 typedef unsigned long long u64;
 
-// probability as 2^-44 fixed point: clamped to [0, 1], NaN is 0
-__device__ __forceinline__ u64 fix(float p) {
-  return __float2ull_rn(fminf(fmaxf(p, 0.f), 1.f) * 17592186044416.f);
+// A probability, clamped to [0, 1] (NaN is 0), as 2^-44 fixed point in two parts: adding 6
+// rounds to a multiple of 2^-21 and leaves that multiple in the mantissa, and the exact
+// remainder (at most 2^-22 either way) plus 1.5 * 2^-21 does the same with 2^-44. Adds and
+// subtracts only: a conversion to 64 bits runs on the special-function unit (with it the
+// verification of 64 requests took 41 us).
+struct Fix {
+  int hi, lo;   // hi * 2^23 + lo, |lo| <= 2^22
+  __device__ __forceinline__ long long value() const { return ((long long)hi << 23) + lo; }
+};
+__device__ __forceinline__ Fix split(float p) {
+  p = fminf(fmaxf(p, 0.f), 1.f);
+  const float u = __fadd_rn(p, 6.f);
+  const float v = __fadd_rn(__fsub_rn(p, __fsub_rn(u, 6.f)), 0x1.8p-21f);
+  return {__float_as_int(u) - 0x40c00000, __float_as_int(v) - 0x35400000};
 }
-__device__ __forceinline__ u64 shfl_u64(u64 x, int src) { return __shfl_sync(0xffffffffu, x, src); }
+__device__ __forceinline__ u64 fix(float p) { return (u64)split(p).value(); }
 __device__ __forceinline__ u64 warp_sum_u64(u64 x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -72,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) oscar_verify_draft_kernel(VerifyPara
   __shared__ int s_par[kTreeNodes], s_tok[kTreeNodes];
   __shared__ u64 s_mass[kTreeNodes];
   __shared__ int s_node, s_ok;
-  __shared__ u64 s_kids, s_warp[kWarps], s_total;
+  __shared__ u64 s_kids, s_warp[kWarps], s_total, s_step[kMaxSteps];
   pdl_wait();
   pdl_trigger();
   const int len = p.draft_len ? p.draft_len[b] : T;
@@ -194,8 +207,39 @@ __global__ void __launch_bounds__(kThreads) oscar_verify_draft_kernel(VerifyPara
       }
     };
     u64 sum = 0;
-#pragma unroll 4
-    for (int at = w0 + 4 * lane; at < w1; at += 128) {
+    // four steps of 128 entries at a time, all loads before the first use; a warp whose
+    // steps reach past the row's ends takes them one by one
+    int at = w0 + 4 * lane;
+    if (!less || qvec) {
+      for (; w0 >= 0 && at - 4 * lane + 512 <= w1; at += 512) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[u] = *reinterpret_cast<const float4*>(row + at + 128 * u);
+          if (less) y[u] = *reinterpret_cast<const float4*>(qrow + at + 128 * u);
+        }
+        int hi = 0, lo = 0;   // at most 16 entries: |lo| < 2^26, hi < 2^26
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          const float ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const Fix f = split(xs[e]);
+            if (less) {
+              const Fix q = split(ys[e]);
+              const long long d = ((long long)(f.hi - q.hi) << 23) + (f.lo - q.lo);
+              sum += d > 0 ? (u64)d : 0;
+            } else {
+              hi += f.hi;
+              lo += f.lo;
+            }
+          }
+        }
+        if (!less) sum += (u64)(((long long)hi << 23) + lo);
+      }
+    }
+    for (; at < w1; at += 128) {
       u64 f[4];
       weights(at, f);
       sum += (f[0] + f[1]) + (f[2] + f[3]);
@@ -238,12 +282,24 @@ __global__ void __launch_bounds__(kThreads) oscar_verify_draft_kernel(VerifyPara
     const double w = (double)fminf(fmaxf(p.u_sample[b], 0.f), 1.f);
     u64 goal = (u64)(w * (double)total);
     if (goal >= total) goal = total - 1;
-    for (int i = 0; i < warp; ++i) before += s_warp[i];
-    if (goal < before || goal >= before + s_warp[warp]) return;
-    for (int base = w0; base < w1; base += 128) {
-      const int at = base + 4 * lane;
-      u64 f[4] = {0, 0, 0, 0};
-      if (at < w1) weights(at, f);
+    // the CTA that holds it: its warps sum the 128-entry steps of the piece, and the first
+    // warp scans the step
+    if (goal < before || goal >= before + s_total) return;
+    int ww = 0;
+    while (goal >= before + s_warp[ww]) before += s_warp[ww++];
+    const int p0 = (rank * kWarps + ww) * per * 128 - skew, p1 = min(p0 + per * 128, V);
+    auto step_weights = [&](int at, u64 (&f)[4]) {
+      float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+      load4(row, at, 0, p1, true, x);
+      if (less) load4(qrow, at, 0, p1, qvec, y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = fix(x[e]);
+        if (less) {
+          const u64 q = fix(y[e]);
+          f[e] = f[e] > q ? f[e] - q : 0;
+        }
+      }
       if (without)
         for (u64 k = kids; k; k &= k - 1) {
           const int out = s_tok[__ffsll((long long)k) - 1] - at;
@@ -251,27 +307,36 @@ __global__ void __launch_bounds__(kThreads) oscar_verify_draft_kernel(VerifyPara
           for (int e = 0; e < 4; ++e)
             if (e == out) f[e] = 0;
         }
-      u64 run = (f[0] + f[1]) + (f[2] + f[3]);
-      const u64 own = run;
+    };
+    for (int i = warp; i < per; i += kWarps) {
+      u64 f[4];
+      step_weights(p0 + 128 * i + 4 * lane, f);
+      const u64 t = warp_sum_u64((f[0] + f[1]) + (f[2] + f[3]));
+      if (lane == 0) s_step[i] = t;
+    }
+    __syncthreads();
+    if (warp) return;
+    int i = 0;
+    while (i + 1 < per && goal >= before + s_step[i]) before += s_step[i++];
+    const int mine = p0 + 128 * i + 4 * lane;
+    u64 f[4];
+    step_weights(mine, f);
+    const u64 own = (f[0] + f[1]) + (f[2] + f[3]);
+    u64 run = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 up = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += up;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + run > goal);
-      if (past) {
-        if (lane == __ffs(past) - 1) {
-          u64 acc = before + run - own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + run > goal);
+    if (past && lane == __ffs(past) - 1) {
+      u64 acc = before + run - own;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool was = acc > goal;
-            acc += f[e];
-            if (!was && acc > goal) p.next_token[b] = at + e;
-          }
-        }
-        return;
+      for (int e = 0; e < 4; ++e) {
+        const bool was = acc > goal;
+        acc += f[e];
+        if (!was && acc > goal) p.next_token[b] = mine + e;
       }
-      before += shfl_u64(run, 31);
     }
     return;
   }
