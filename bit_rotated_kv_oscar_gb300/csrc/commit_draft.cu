@@ -9,11 +9,18 @@
 // accepted is known to the device only, so the counts and row indices are read
 // there and every request may append a different number.
 //
-// CTA (x, h) takes KV head h of requests x, x + gridDim.x, ...: the head's two
-// rotations (128 KiB) are staged in shared memory once, and the rows to quantise
-// are rotated eight at a time, so that one shared-memory read of a rotation entry
-// feeds eight FMAs. The sums keep the append kernel's order (two chains of 64 terms
-// per channel, then their sum), which the byte equality needs.
+// CTA (x, h, kind) takes the keys or the values of KV head h of requests x, x + gridDim.x,
+// ..., sixteen at a time: one warp reads and checks one request's state, count and path. The
+// rotation (64 KiB) is staged in shared memory once, two CTAs per SM, and the rows that
+// all of these requests quantise are rotated sixteen at a time, eight to a thread, so that
+// one shared-memory read of a rotation entry feeds eight FMAs; the next sixteen are on
+// their way meanwhile. The sums keep the append kernel's order (two chains of 64 terms per
+// channel, then their sum), which the byte equality needs.
+//
+// Bound: latency (state, rows, rotation, stores follow one another); the rotation itself is
+// 4 * 128 * 128 flops per row and head.
+#include <type_traits>
+
 #include "oscar_internal.cuh"
 #include "token_quant.cuh"
 #include "warp_mma.cuh"
@@ -22,138 +29,185 @@ namespace oscar {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRows = 8;                    // rows rotated at once
+constexpr int kReqs = kThreads / 32;        // requests read at once
+constexpr int kRows = 16;                   // rows rotated at once
 constexpr int kMat = kHeadDim * kHeadDim;
 struct CommitSmem {
-  float rot[2][kMat];                       // R_K[h], R_V[h]
-  float x[kRows][2][kHeadDim];              // rows being quantised, K and V
-  float red[kRows][2][2][kHeadDim];         // their rotations, two half sums per channel
-  uint8_t codes[kRows][2][kHeadDim];
+  float rot[kMat];                          // R_K[h] or R_V[h]
+  float x[kRows][kHeadDim];                 // rows being quantised
+  float red[kRows][2][kHeadDim];            // their rotations, two half sums per channel
+  __nv_bfloat16 raw[2][kRows][kHeadDim];    // the same rows as they lie in the cache or the draft, and the next
+  uint8_t codes[kRows][2][kHeadDim];        // one kind's is used (store_token_block's layout)
   __half meta[kRows][2][kGroups][2];
-  int path[kTreeNodes];
+  int path[kReqs][kTreeNodes];
+  int n[kReqs], L[kReqs], E[kReqs], row[kReqs];   // accepted rows, state and window row; n = 0: nothing to do
+  int first[kReqs + 1];                     // rows to quantise before each request
+  int page[2][kRows];                       // page ids of the rows in raw
 };
 
-__global__ void __launch_bounds__(kThreads, 1) oscar_commit_draft_kernel(CommitParams p) {
+__global__ void __launch_bounds__(kThreads, 2) oscar_commit_draft_kernel(CommitParams p) {
   extern __shared__ __align__(16) uint8_t dsm[];
   CommitSmem& sm = *reinterpret_cast<CommitSmem*>(dsm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, kind = blockIdx.z;
   const int S = p.sink, W = p.recent, Hkv = p.num_kv_heads, ng = p.ngroups;
   // constant data before the wait
-  const float* rk = p.R_K + (size_t)h * kMat;
-  const float* rv = p.R_V + (size_t)h * kMat;
-  const uint32_t srot = (uint32_t)__cvta_generic_to_shared(&sm.rot[0][0]);
-  for (int i = tid; i < kMat / 4; i += kThreads) {
-    wm::cp_async16(srot + 16 * i, rk + 4 * i);
-    if (!p.fold_rv) wm::cp_async16(srot + kMat * 4 + 16 * i, rv + 4 * i);
-  }
+  const float* rot = (kind ? p.R_V : p.R_K) + (size_t)h * kMat;
+  const bool fold = kind && p.fold_rv;   // the values arrive in the R_V basis
+  const uint32_t srot = (uint32_t)__cvta_generic_to_shared(&sm.rot[0]);
+  if (!fold)
+    for (int i = tid; i < kMat / 4; i += kThreads) wm::cp_async16(srot + 16 * i, rot + 4 * i);
   wm::cp_commit();
   pdl_wait();
   pdl_trigger();
-  bool staged = false;
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    __syncthreads();   // the previous request's shared data is consumed
-    const oscar_seq_state st = p.state[b];
-    const int n = p.count[b];
-    bool good = n >= 0 && n <= p.nodes;
-    if (good && tid < n) {
-      const int r = p.path[(size_t)b * p.nodes + tid];
-      sm.path[tid] = r;
-      good = r >= 0 && r < p.nodes;
-    }
-    const bool path_ok = __syncthreads_and(good);
-    const bool seq_ok = state_ok(st, S, W, p.max_batch);
-    if (tid == 0) {
-      // the last of the request's Hkv CTAs to have read its state publishes the
-      // new one: each reads it before taking its ticket
-      asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
-      if (atomicAdd(p.tickets + b, 1u) == (unsigned)Hkv - 1u) {
-        asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
-        if (path_ok && seq_ok) {
-          const int64_t nl = (int64_t)st.seq_len + n, ne = nl - W;
-          oscar_seq_state out = st;
-          out.seq_len = (int32_t)nl;
-          out.int2_end = (int32_t)(ne > max(st.int2_end, S) ? ne : max(st.int2_end, S));
-          p.state[b] = out;
-        } else {
-          atomicOr(p.err_flags, (path_ok ? 0u : OSCAR_FLAG_BAD_TREE) | (seq_ok ? 0u : OSCAR_FLAG_BAD_STATE));
+  const float clip = (kind ? p.clip_V : p.clip_K)[h];
+  const size_t slots = (size_t)(S + W);
+  const __nv_bfloat16* input = kind ? p.v : p.k;
+  auto window_of = [&](int q) { return p.window + (((size_t)sm.row[q] * Hkv + h) * 2 + kind) * slots * kHeadDim; };
+  for (int b0 = blockIdx.x; b0 < p.batch; b0 += kReqs * gridDim.x) {
+    auto request = [&](int q) { return b0 + q * (int)gridDim.x; };
+    __syncthreads();   // the previous requests' shared data is consumed
+    oscar_seq_state out{};   // this warp's request afterwards
+    uint32_t bad = 0u;
+    {
+      const int b = request(warp);
+      int n = 0, m = 0;
+      if (b < p.batch) {
+        const oscar_seq_state st = p.state[b];
+        const int c = p.count[b];
+        bool good = c >= 0 && c <= p.nodes;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = lane + 32 * e;
+          if (i < p.nodes) {
+            const int r = p.path[(size_t)b * p.nodes + i];
+            sm.path[warp][i] = r;
+            if (i < c) good = good && r >= 0 && r < p.nodes;
+          }
         }
-        p.tickets[b] = 0u;
+        const bool path_ok = __all_sync(0xffffffffu, good), seq_ok = state_ok(st, S, W, p.max_batch);
+        if (path_ok && seq_ok) n = c;
+        const int64_t nl = (int64_t)st.seq_len + n, ne = nl - W;
+        const int e0 = st.int2_end, e1 = max(e0, S);   // state_ok: int2_end >= sink
+        const int e2 = (int)(ne > e1 ? ne : e1);
+        m = n > 0 ? e2 - e0 : 0;
+        if (lane == 0) {
+          sm.L[warp] = st.seq_len;
+          sm.E[warp] = e0;
+          sm.row[warp] = st.window_row;
+        }
+        out = st;
+        out.seq_len = (int32_t)nl;
+        out.int2_end = e2;
+        bad = (path_ok ? 0u : OSCAR_FLAG_BAD_TREE) | (seq_ok ? 0u : OSCAR_FLAG_BAD_STATE);
+      }
+      if (lane == 0) {
+        sm.n[warp] = n;
+        sm.first[warp + 1] = m;
       }
     }
-    if (!path_ok || !seq_ok || n == 0) continue;
-    const int64_t L = st.seq_len, E = st.int2_end;
-    int64_t E2 = L + n - W;
-    if (E2 < E) E2 = E;
-    if (E2 < S) E2 = S;
-    const size_t slots = (size_t)(S + W);
-    __nv_bfloat16* win = p.window + ((size_t)st.window_row * Hkv + h) * 2 * slots * kHeadDim;   // K rows, then V rows
-    const int m = (int)(E2 - E);   // rows to quantise: positions E .. E2 - 1, at most n
-    if (m > 0 && !staged) {
-      wm::cp_wait<0>();
-      staged = true;   // visible to the other threads after the barrier below
+    __syncthreads();
+    if (warp == 0) {
+      int m = lane < kReqs ? sm.first[lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < kReqs; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane >= o) m += up;
+      }
+      if (lane < kReqs) sm.first[lane + 1] = m;
+      if (lane == 0) sm.first[0] = 0;
     }
-    for (int i0 = 0; i0 < m; i0 += kRows) {
-      const int rows = min(kRows, m - i0);
-      // 8 rows x 2 kinds x 128 channels, 4 channels per thread
-      for (int i = tid; i < rows * 64; i += kThreads) {
-        const int r = i >> 6, kind = (i >> 5) & 1, c = 4 * (i & 31);
-        const int64_t pos = E + i0 + r;
-        const __nv_bfloat16* src;
-        if (pos < L)
-          src = win + (kind * slots + S + pos % W) * kHeadDim + c;
-        else
-          src = (kind ? p.v : p.k) + (((size_t)b * p.nodes + sm.path[pos - L]) * Hkv + h) * kHeadDim + c;
-        const uint2 w = *reinterpret_cast<const uint2*>(src);
-        *reinterpret_cast<float4*>(&sm.x[r][kind][c]) =
+    __syncthreads();
+    const int M = sm.first[kReqs];
+    auto request_of = [&](int r) {   // of row r of the M
+      int q = 0;
+      while (r >= sm.first[q + 1]) ++q;
+      return q;
+    };
+    auto fetch = [&](int r0, int buf) {   // rows r0 .. of the M: 16-byte pieces
+      for (int i = tid; i < min(kRows, M - r0) * 16; i += kThreads) {
+        const int r = i >> 4, c = 8 * (i & 15), q = request_of(r0 + r);
+        const int pos = sm.E[q] + (r0 + r - sm.first[q]), L = sm.L[q];
+        const __nv_bfloat16* src =
+            pos < L ? window_of(q) + (size_t)(S + pos % W) * kHeadDim + c
+                    : input + (((size_t)request(q) * p.nodes + sm.path[q][pos - L]) * Hkv + h) * kHeadDim + c;
+        wm::cp_async16((uint32_t)__cvta_generic_to_shared(&sm.raw[buf][r][c]), src);
+        if ((i & 15) == 0) {
+          const int pidx = pos / kPage;
+          if (pidx < p.pt_stride)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"((uint32_t)__cvta_generic_to_shared(&sm.page[buf][r])),
+                         "l"(p.page_table + (size_t)request(q) * p.pt_stride + pidx));
+          else
+            sm.page[buf][r] = -1;
+        }
+      }
+      wm::cp_commit();
+    };
+    if (M > 0) fetch(0, 0);
+    for (int r0 = 0, buf = 0; r0 < M; r0 += kRows, buf ^= 1) {
+      const int rows = min(kRows, M - r0);
+      if (r0 + kRows < M) {
+        fetch(r0 + kRows, buf ^ 1);
+        wm::cp_wait<1>();
+      } else {
+        wm::cp_wait<0>();
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * 32; i += kThreads) {
+        const uint2 w = reinterpret_cast<const uint2*>(&sm.raw[buf][0][0])[i];
+        reinterpret_cast<float4*>(&sm.x[0][0])[i] =
             make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                         __uint_as_float(w.y & 0xffff0000u));
       }
       __syncthreads();
       {
-        // thread (kind, half, channel c): 64 terms of x R in order, for every row
-        const int kind = tid >> 8, half = (tid >> 7) & 1, c = tid & 127, k0 = 64 * half;
-        if (kind == 1 && p.fold_rv) {
-          for (int r = 0; r < rows; ++r) sm.red[r][1][half][c] = half ? 0.f : sm.x[r][1][c];
-        } else {
-          float acc[kRows] = {};
-          const float* R = sm.rot[kind] + k0 * kHeadDim + c;
+        // thread (rows 8 g .., half, channel c): 64 terms of x R in order, for each row
+        const int g = tid >> 8, half = (tid >> 7) & 1, c = tid & 127, k0 = 64 * half, n = rows - 8 * g;
+        if (fold) {
+          for (int r = 8 * g; r < min(rows, 8 * g + 8); ++r) sm.red[r][half][c] = half ? 0.f : sm.x[r][c];
+        } else if (n > 0) {
+          const float* R = sm.rot + k0 * kHeadDim + c;
+          auto rotate = [&](auto count) {
+            constexpr int N = decltype(count)::value;
+            float acc[N] = {};
 #pragma unroll 4
-          for (int i = 0; i < 64; i += 4) {
-            const float r0 = R[i * kHeadDim], r1 = R[(i + 1) * kHeadDim], r2 = R[(i + 2) * kHeadDim],
-                        r3 = R[(i + 3) * kHeadDim];
+            for (int i = 0; i < 64; i += 4) {
+              const float v0 = R[i * kHeadDim], v1 = R[(i + 1) * kHeadDim], v2 = R[(i + 2) * kHeadDim],
+                          v3 = R[(i + 3) * kHeadDim];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-              if (r < rows) {
-                const float4 x = *reinterpret_cast<const float4*>(&sm.x[r][kind][k0 + i]);
-                acc[r] = fmaf(x.x, r0, acc[r]);
-                acc[r] = fmaf(x.y, r1, acc[r]);
-                acc[r] = fmaf(x.z, r2, acc[r]);
-                acc[r] = fmaf(x.w, r3, acc[r]);
+              for (int r = 0; r < N; ++r) {
+                const float4 x = *reinterpret_cast<const float4*>(&sm.x[8 * g + r][k0 + i]);
+                acc[r] = fmaf(x.x, v0, acc[r]);
+                acc[r] = fmaf(x.y, v1, acc[r]);
+                acc[r] = fmaf(x.z, v2, acc[r]);
+                acc[r] = fmaf(x.w, v3, acc[r]);
               }
             }
-          }
 #pragma unroll
-          for (int r = 0; r < kRows; ++r)
-            if (r < rows) sm.red[r][kind][half][c] = acc[r];
+            for (int r = 0; r < N; ++r) sm.red[8 * g + r][half][c] = acc[r];   // rows past the last are not used
+          };
+          if (n > 4) rotate(std::integral_constant<int, 8>());
+          else if (n > 1) rotate(std::integral_constant<int, 4>());
+          else rotate(std::integral_constant<int, 1>());
         }
       }
       __syncthreads();
-      // warp item (row, kind, 64 channels): clip, group extremes, scale, zero, codes
-      for (int it = warp; it < rows * 4; it += kThreads / 32) {
-        const int r = it >> 2, kind = (it >> 1) & 1, c = 64 * (it & 1) + lane;
-        const float clip = (kind ? p.clip_V : p.clip_K)[h];
+      // warp item (row, 64 channels): clip, group extremes, scale, zero, codes
+      for (int it = warp; it < rows * 2; it += kThreads / 32) {
+        const int r = it >> 1, c = 64 * (it & 1) + lane;
         float x[2], mn[2], mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float v = sm.red[r][kind][0][c + 32 * e] + sm.red[r][kind][1][c + 32 * e];
+          const float v = sm.red[r][0][c + 32 * e] + sm.red[r][1][c + 32 * e];
           x[e] = fminf(fmaxf(v, -clip), clip);
           mn[e] = mx[e] = x[e];
+        }
 #pragma unroll
-          for (int o = 16; o; o >>= 1) {
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], o));
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
           }
-        }
         if (ng != kGroups) {
           mn[0] = mn[1] = fminf(mn[0], mn[1]);
           mx[0] = mx[1] = fmaxf(mx[0], mx[1]);
@@ -173,26 +227,49 @@ __global__ void __launch_bounds__(kThreads, 1) oscar_commit_draft_kernel(CommitP
       __syncthreads();
       for (int r = tid >> 7; r < rows; r += kThreads / 128) {
         const int role = tid & 127;
-        if (role < 72) {
-          const int64_t pos = E + i0 + r, pidx = pos / kPage;
-          const int id = pidx < p.pt_stride ? p.page_table[(size_t)b * p.pt_stride + pidx] : -1;
+        // the roles of this kind: K codes 0 .. 7, metadata 64 .. 67; V codes 32 .. 47, metadata 68 .. 71
+        if (kind ? (role >= 32 && role < 48) || (role >= 68 && role < 72) : role < 8 || (role >= 64 && role < 68)) {
+          const int q = request_of(r0 + r), pos = sm.E[q] + (r0 + r - sm.first[q]), id = sm.page[buf][r];
           if (id >= 0 && id < p.num_pages)
-            store_token_block(p.pool + ((size_t)id * Hkv + h) * block_bytes(ng), (int)(pos % kPage), role, ng, sm.codes[r],
-                              sm.meta[r]);
-          else if (role == 0)
+            store_token_block(p.pool + ((size_t)id * Hkv + h) * block_bytes(ng), pos % kPage, role, ng, sm.codes[r], sm.meta[r]);
+          else if (role == 0 || role == 32)
             atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
         }
       }
-      __syncthreads();
+      __syncthreads();   // the next fetch overwrites the page ids read here
     }
-    // every ring entry that leaves has been read: the new rows take their places
-    for (int i = tid; i < n * 32; i += kThreads) {
-      const int j = i >> 5, kind = (i >> 4) & 1, c = 8 * (i & 15);
-      const int64_t pos = L + j;
-      if (pos < S || pos >= E2) {
-        const size_t slot = pos < S ? pos : S + pos % W;
-        *reinterpret_cast<uint4*>(win + (kind * slots + slot) * kHeadDim + c) = *reinterpret_cast<const uint4*>(
-            (kind ? p.v : p.k) + (((size_t)b * p.nodes + sm.path[j]) * Hkv + h) * kHeadDim + c);
+    __syncthreads();
+    // every ring entry that leaves has been read: the new rows take their places. A
+    // half-warp per row (16 pieces of 16 bytes), four rows' loads before their stores
+    const int nreq = min(kReqs, (p.batch - b0 + (int)gridDim.x - 1) / (int)gridDim.x), nrows = nreq * p.nodes;
+    for (int i0 = tid >> 4; i0 < nrows; i0 += 4 * (kThreads / 16)) {
+      uint4 x[4];
+      __nv_bfloat16* dst[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * (kThreads / 16), q = i / p.nodes, j = i - q * p.nodes, c = 8 * (tid & 15);
+        dst[u] = nullptr;
+        if (i >= nrows || j >= sm.n[q]) continue;
+        const int pos = sm.L[q] + j, e2 = sm.E[q] + (sm.first[q + 1] - sm.first[q]);
+        if (pos >= S && pos < e2) continue;
+        dst[u] = window_of(q) + (size_t)(pos < S ? pos : S + pos % W) * kHeadDim + c;
+        x[u] = *reinterpret_cast<const uint4*>(
+            input + (((size_t)request(q) * p.nodes + sm.path[q][j]) * Hkv + h) * kHeadDim + c);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
+    }
+    // the last of a request's 2 Hkv CTAs to have read its state publishes the new one: each
+    // reads it before taking its ticket
+    if (lane == 0 && request(warp) < p.batch) {
+      const int b = request(warp);
+      asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
+      if (atomicAdd(p.tickets + b, 1u) == 2u * Hkv - 1u) {
+        asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
+        if (bad) atomicOr(p.err_flags, bad);
+        else p.state[b] = out;
+        p.tickets[b] = 0u;
       }
     }
   }
@@ -207,9 +284,9 @@ cudaError_t launch_commit_draft(const CommitParams& p, int num_sms, cudaStream_t
     return cudaFuncSetAttribute(oscar_commit_draft_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(CommitSmem));
   });
   if (ea != cudaSuccess) return ea;
-  int nx = num_sms / p.num_kv_heads;   // one CTA per SM
+  int nx = num_sms / p.num_kv_heads;   // two CTAs per SM, keys and values
   nx = nx < 1 ? 1 : (nx > p.batch ? p.batch : nx);
-  const cudaError_t e = launch_pdl(oscar_commit_draft_kernel, dim3((unsigned)nx, (unsigned)p.num_kv_heads), dim3(kThreads),
+  const cudaError_t e = launch_pdl(oscar_commit_draft_kernel, dim3((unsigned)nx, (unsigned)p.num_kv_heads, 2), dim3(kThreads),
                                    sizeof(CommitSmem), s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
