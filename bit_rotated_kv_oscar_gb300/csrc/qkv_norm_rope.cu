@@ -20,34 +20,38 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = kHeadDim / 2;
-constexpr int kTokensPerCta = 4;
+constexpr int kTokensPerCta = 8;
+constexpr int kUnroll = 5;               // heads of a half-warp in flight
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void unpack4(const uint2& w, float* x) {
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xffff0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xffff0000u);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&r);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
+__device__ __forceinline__ uint2 pack4(const float* x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// CTA: `tpc` tokens; half-warp per head, 8 channels per lane. The launch uses no
-// early trigger: what follows may read q, k and v as soon as it starts.
-__global__ void __launch_bounds__(kThreads) oscar_qkv_norm_rope_kernel(RopeParams p, int tpc) {
-  __shared__ float2 cs[kTokensPerCta][kMaxPairs];
+// CTA: `tpc` tokens; half-warp per head, lane = two blocks of 4 channels. A rotated lane's
+// blocks are the two sides of 4 pairs, so that no value crosses lanes but the norm's sum
+// (the instruction count, not the loads, set the pace of a version with shuffled partners).
+// The launch uses no early trigger: what follows may read q, k and v as soon as it starts.
+template <bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 4) oscar_qkv_norm_rope_kernel(RopeParams p, int tpc) {
+  __shared__ __align__(16) float2 cs[kTokensPerCta][kMaxPairs];
   const int tid = threadIdx.x, sub = tid & 15, hw = tid >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * tpc;
   const int nt = (int)min((int64_t)tpc, p.tokens - t0);
-  const int half = p.rotary / 2, heads = p.num_q_heads + 2 * p.num_kv_heads;
+  const int half = p.rotary / 2, nq = p.num_q_heads, nk = p.num_kv_heads, heads = nq + 2 * nk;
+  // channels of the lane's blocks: half-split pairs (i, i + half); the channels past
+  // `rotary`, and with neighbours as pairs all channels, in order
+  const int lo_lanes = half / 4;
+  const bool turned = INTERLEAVED ? 8 * sub < p.rotary : sub < lo_lanes;
+  const int ca = INTERLEAVED ? 8 * sub : sub < lo_lanes ? 4 * sub : p.rotary + 8 * (sub - lo_lanes);
+  const int cb = INTERLEAVED || !turned ? ca + 4 : ca + half;
+  const uint32_t mask = 0xffffu << (tid & 16);   // this half-warp
   pdl_wait();
   for (int i = tid; i < nt * half; i += kThreads) {
     const int t = i / half, c = i - t * half;
@@ -56,61 +60,72 @@ __global__ void __launch_bounds__(kThreads) oscar_qkv_norm_rope_kernel(RopeParam
     sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &co);   // 2^-31: half turns
     cs[t][c] = make_float2(co, s);
   }
-  __syncthreads();
-  float w[2][8];
+  uint2 w[2][2] = {};   // packed: the query and the key weights of the lane's blocks
   if (p.q_weight) {
-    unpack8(*reinterpret_cast<const uint4*>(p.q_weight + 8 * sub), w[0]);
-    unpack8(*reinterpret_cast<const uint4*>(p.k_weight + 8 * sub), w[1]);
+    w[0][0] = *reinterpret_cast<const uint2*>(p.q_weight + ca);
+    w[0][1] = *reinterpret_cast<const uint2*>(p.q_weight + cb);
+    w[1][0] = *reinterpret_cast<const uint2*>(p.k_weight + ca);
+    w[1][1] = *reinterpret_cast<const uint2*>(p.k_weight + cb);
   }
-  // half-split pairs: channels below `half` pair with lane + half / 8, the others back
-  const int c0 = 8 * sub;
-  const bool turned = c0 < p.rotary, low = c0 < half;
-  const int partner = p.interleaved || !turned ? sub : (low ? sub + half / 8 : sub - half / 8);
-  const int lane_partner = (tid & 16) | partner;
-  for (int i = hw; i < nt * heads; i += kThreads / 16) {
-    const int t = i / heads, hd = i - t * heads;
-    const int64_t tok = t0 + t;
-    const uint4 in = *reinterpret_cast<const uint4*>(p.qkv + tok * p.row_stride + (int64_t)hd * kHeadDim + c0);
-    if (hd >= p.num_q_heads + p.num_kv_heads) {
-      const int64_t at = tok * p.num_kv_heads + (hd - p.num_q_heads - p.num_kv_heads);
-      *reinterpret_cast<uint4*>(p.v + at * kHeadDim + c0) = in;
-      continue;
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    const __nv_bfloat16* src = p.qkv + (t0 + t) * p.row_stride;
+    __nv_bfloat16* qd = p.q + (t0 + t) * nq * kHeadDim;
+    __nv_bfloat16* kd = p.k + (t0 + t) * nk * kHeadDim;
+    __nv_bfloat16* vd = p.v + (t0 + t) * nk * kHeadDim;
+    float co[4] = {1.f, 1.f, 1.f, 1.f}, si[4] = {0.f, 0.f, 0.f, 0.f};
+    if (turned) {
+      const float4* c4 = reinterpret_cast<const float4*>(&cs[t][4 * sub]);
+      const float4 u = c4[0], v = c4[1];
+      co[0] = u.x, si[0] = u.y, co[1] = u.z, si[1] = u.w;
+      co[2] = v.x, si[2] = v.y, co[3] = v.z, si[3] = v.w;
     }
-    const bool isk = hd >= p.num_q_heads;
-    const uint32_t mask = 0xffffu << (tid & 16);   // this half-warp
-    float x[8];
-    unpack8(in, x);
-    if (p.q_weight) {
-      float ss = 0.f;
+    for (int h0 = hw; h0 < heads; h0 += kUnroll * (kThreads / 16)) {
+      uint2 in[kUnroll][2];   // all loads before the first use
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      const float r = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (isk ? w[1][e] : w[0][e]);
-    }
-    float y[8];
-    if (p.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = turned ? cs[t][4 * sub + e] : make_float2(1.f, 0.f);
-        y[2 * e] = x[2 * e] * a.x - x[2 * e + 1] * a.y;
-        y[2 * e + 1] = x[2 * e + 1] * a.x + x[2 * e] * a.y;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = h0 + u * (kThreads / 16);
+        if (h < heads) {
+          in[u][0] = *reinterpret_cast<const uint2*>(src + h * kHeadDim + ca);
+          in[u][1] = *reinterpret_cast<const uint2*>(src + h * kHeadDim + cb);
+        }
       }
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float other = __shfl_sync(mask, x[e], lane_partner);
-        const float2 a = turned ? cs[t][(low ? c0 : c0 - half) + e] : make_float2(1.f, 0.f);
-        y[e] = turned ? fmaf(x[e], a.x, low ? -other * a.y : other * a.y) : x[e];
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = h0 + u * (kThreads / 16);
+        if (h >= heads) break;
+        __nv_bfloat16* dst = h < nq ? qd + h * kHeadDim : h < nq + nk ? kd + (h - nq) * kHeadDim : vd + (h - nq - nk) * kHeadDim;
+        if (h < nq + nk) {
+          float x[8];
+          unpack4(in[u][0], x);
+          unpack4(in[u][1], x + 4);
+          if (p.q_weight) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+            const float r = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
+            float wf[8];
+            unpack4(h < nq ? w[0][0] : w[1][0], wf);
+            unpack4(h < nq ? w[0][1] : w[1][1], wf + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wf[e];
+          }
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int a = INTERLEAVED ? 2 * e : e, b = INTERLEAVED ? 2 * e + 1 : e + 4;
+            y[a] = fmaf(x[a], co[e], -x[b] * si[e]);
+            y[b] = fmaf(x[b], co[e], x[a] * si[e]);
+          }
+          in[u][0] = pack4(y);
+          in[u][1] = pack4(y + 4);
+        }
+        *reinterpret_cast<uint2*>(dst + ca) = in[u][0];
+        *reinterpret_cast<uint2*>(dst + cb) = in[u][1];
       }
     }
-    const uint4 out = pack8(y);
-    if (isk)
-      *reinterpret_cast<uint4*>(p.k + (tok * p.num_kv_heads + (hd - p.num_q_heads)) * kHeadDim + c0) = out;
-    else
-      *reinterpret_cast<uint4*>(p.q + (tok * p.num_q_heads + hd) * kHeadDim + c0) = out;
   }
 }
 
@@ -119,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) oscar_qkv_norm_rope_kernel(RopeParam
 cudaError_t launch_qkv_norm_rope(const RopeParams& p, cudaStream_t s) {
   const int tpc = p.tokens >= 4096 ? kTokensPerCta : 1;
   const int64_t ctas = (p.tokens + tpc - 1) / tpc;
-  const cudaError_t e = launch_pdl(oscar_qkv_norm_rope_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, s, p, tpc);
+  const cudaError_t e = launch_pdl(p.interleaved ? oscar_qkv_norm_rope_kernel<true> : oscar_qkv_norm_rope_kernel<false>, dim3((unsigned)ctas), dim3(kThreads), 0, s, p, tpc);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
