@@ -13,9 +13,6 @@
 
 #include "oscar_internal.cuh"
 #include "tree_attn.cuh"
-#ifndef OSCAR_TREE_WARP_ROWS
-#define OSCAR_TREE_WARP_ROWS 32
-#endif
 
 using namespace oscar;
 
@@ -606,15 +603,38 @@ static TreePlan tree_plan(const oscar_ctx* ctx, int batch, int nodes) {
   TreePlan t{};
   const int hkv = ctx->cfg.num_kv_heads;
   t.rows = nodes * (ctx->cfg.num_q_heads / hkv);
-  t.tile_rows = t.rows <= 16 ? 16 : (t.rows <= OSCAR_TREE_WARP_ROWS ? 32 : 2 * kWideRows);
-  t.col_tiles = (t.rows + t.tile_rows - 1) / t.tile_rows;
   t.row_tiles = (t.rows + 31) / 32;
   t.images128 = (t.rows + kWideRows - 1) / kWideRows;
   t.win_slots = (ctx->cfg.sink + ctx->cfg.recent + nodes + kTreeWindowChunk - 1) / kTreeWindowChunk;
-  // one wave of CTAs together with the BF16 ones, at most kSplitPages pages per CTA
-  const int64_t units = (int64_t)batch * hkv * t.col_tiles, pages = ctx->cfg.max_pages_per_seq;
-  const int64_t ctas = (t.tile_rows == 16 ? 2 : 1) * (int64_t)ctx->num_sms;
-  int64_t s = std::max((ctas - units * t.win_slots) / units, (pages + kSplitPages - 1) / kSplitPages);
+  const int64_t pages = ctx->cfg.max_pages_per_seq;
+  // splits that fill one wave together with the BF16 CTAs, with per_sm resident CTAs
+  auto one_wave = [&](int per_sm) {
+    const int64_t units = (int64_t)batch * hkv * t.col_tiles;
+    return (per_sm * (int64_t)ctx->num_sms - units * t.win_slots) / units;
+  };
+  auto tiles = [&](int rows) {
+    t.tile_rows = rows;
+    t.col_tiles = (t.rows + rows - 1) / rows;
+  };
+  int64_t s;
+  if (t.rows > 32) {
+    // tensor-memory kernel, one CTA per SM: its fixed cost (operands, 512 columns, merge of
+    // eight warps' rows) asks for long splits
+    tiles(2 * kWideRows);
+    s = std::max(one_wave(1), (pages + kSplitPages - 1) / kSplitPages);
+  } else {
+    // Warp tiles. A call whose single wave leaves a CTA at most 128 pages is bound by latency
+    // and takes 16-row tiles (1 x 4099 tokens, 20 rows: 19.2 us against 21.4); else 17 .. 32
+    // rows go to the pair kernel (28 x 100k, 32 rows: 1346 us against 1538), in about five
+    // waves, so that ragged requests and the last wave leave few SMs idle.
+    tiles(16);
+    s = one_wave(2);
+    if (s < 1 || pages > 128 * s) {
+      tiles(t.rows <= 16 ? 16 : 32);
+      const int64_t units = (int64_t)batch * hkv * t.col_tiles;
+      s = std::max({one_wave(2), (10 * (int64_t)ctx->num_sms + units - 1) / units, (pages + kSplitPages - 1) / kSplitPages});
+    }
+  }
   s = std::min<int64_t>(s, (pages + 7) / 8);   // >= 8 pages per split: one per warp
   if (ctx->cfg.num_splits > 0) s = ctx->cfg.num_splits;
   t.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 256));

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kRotThreads) oscar_tree_rotate_kernel(TreePara
 }
 
 // --------------------------------------------------------------------------
-// 2. attention over a slice of the keys for MT x 16 query rows
+// 2. attention over a slice of the keys for 16 query rows
 // --------------------------------------------------------------------------
 // The query rows are the row operand, tokens the columns of the score product and
 // the reduction of the value product, so the probabilities of the score
@@ -215,17 +215,25 @@ __global__ void __launch_bounds__(kRotThreads) oscar_tree_rotate_kernel(TreePara
 // (token 8 th + gid, channels 16 i + 8 x + 2 tig, + 1 in slot i) are the column
 // fragments b_x of token tile th; its V words (tokens 8 tt + 2 tig, + 1, channel
 // 16 i + 8 x + gid) the fragments b_tt of channel tile (i, x).
-template <int MT>
 struct State {
-  float o[MT][8][2][4];   // value sums: channels 16 i + 8 x + 2 tig, + 1 of rows gid (0, 1) and gid + 8 (2, 3)
-  float oz[MT][4];        // columns 0 .. NG-1: value zero-point sums of the groups, column 4: the denominator
-  float m[MT][2];         // running (lazy) maxima of rows gid, gid + 8, in score units
+  float o[8][2][4];   // value sums: channels 16 i + 8 x + 2 tig, + 1 of rows gid (0, 1) and gid + 8 (2, 3)
+  float oz[4];        // columns 0 .. NG-1: value zero-point sums of the groups, column 4: the denominator
+  float m[2];         // running (lazy) maxima of rows gid, gid + 8, in score units
+  __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) oz[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.f;
+  }
 };
 
-// scores of one page in score units: u[mt][th] tokens 8 th + 2 tig, + 1 of rows gid, gid + 8
-template <int NG, int MT>
-__device__ __forceinline__ void page_scores(const uint8_t* sb, const uint4* qs, const uint2 (&zs)[MT], int lane,
-                                            float (&u)[MT][2][4]) {
+// scores of one page in score units: u[th] tokens 8 th + 2 tig, + 1 of rows gid, gid + 8.
+// The codes are exact operands: a group's products are summed, then scaled
+template <int NG>
+__device__ __forceinline__ void page_scores(const uint8_t* sb, const uint4* qs, uint2 zs, int lane, float (&u)[2][4]) {
   const int gid = lane >> 2, tig = lane & 3;
   const uint4 kw = *reinterpret_cast<const uint4*>(sb + lane * 16);
   const uint4 kh = shr10(kw);
@@ -233,101 +241,74 @@ __device__ __forceinline__ void page_scores(const uint8_t* sb, const uint4* qs, 
     const int zo = kzero_off(NG, gid, NG == kGroups ? 2 * (tig & 1) : 0);
     constexpr int step = kzero_off(NG, 8, 0) - kzero_off(NG, 0, 0);
     const bool on = NG == kGroups || tig < 2;
-    const uint32_t z0 = on ? *reinterpret_cast<const uint32_t*>(sb + zo) : 0u;
-    const uint32_t z1 = on ? *reinterpret_cast<const uint32_t*>(sb + zo + step) : 0u;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      mma1688_z(u[mt][0], zs[mt], z0);
-      mma1688_z(u[mt][1], zs[mt], z1);
-    }
+    mma1688_z(u[0], zs, on ? *reinterpret_cast<const uint32_t*>(sb + zo) : 0u);
+    mma1688_z(u[1], zs, on ? *reinterpret_cast<const uint32_t*>(sb + zo + step) : 0u);
   }
   const uint8_t* s0 = sb + kscale_off(NG, 2 * tig, 0);   // tokens 2 tig (+ 8): next, tokens 2 tig + 1 (+ 8)
 #pragma unroll
   for (int gq = 0; gq < NG; ++gq) {
-    float c[MT][2][4];
-#define OSCAR_QK(I, FIRST)                                                             \
-  {                                                                                    \
-    const uint32_t x0 = slot_bits<I>(kw.x, kh.x), x1 = slot_bits<I>(kw.y, kh.y);       \
-    const uint32_t y0 = slot_bits<I>(kw.z, kh.z), y1 = slot_bits<I>(kw.w, kh.w);       \
-    _Pragma("unroll") for (int mt = 0; mt < MT; ++mt) {                                \
-      const uint4 a = qs[(mt * 8 + (I)) * 32 + lane];                                  \
-      if (FIRST) {                                                                     \
-        mma16816_z(c[mt][0], a, x0, x1);                                               \
-        mma16816_z(c[mt][1], a, y0, y1);                                               \
-      } else {                                                                         \
-        mma16816(c[mt][0], a, x0, x1);                                                 \
-        mma16816(c[mt][1], a, y0, y1);                                                 \
-      }                                                                                \
-    }                                                                                  \
+    float c[2][4];
+#define OSCAR_QK(I, MMA)                                              \
+  {                                                                   \
+    const uint4 a = qs[(I) * 32 + lane];                              \
+    MMA(c[0], a, slot_bits<I>(kw.x, kh.x), slot_bits<I>(kw.y, kh.y)); \
+    MMA(c[1], a, slot_bits<I>(kw.z, kh.z), slot_bits<I>(kw.w, kh.w)); \
   }
     if constexpr (NG == kGroups) {
-      if (gq == 0) { OSCAR_QK(0, true) OSCAR_QK(1, false) }
-      if (gq == 1) { OSCAR_QK(2, true) OSCAR_QK(3, false) }
-      if (gq == 2) { OSCAR_QK(4, true) OSCAR_QK(5, false) }
-      if (gq == 3) { OSCAR_QK(6, true) OSCAR_QK(7, false) }
+      if (gq == 0) { OSCAR_QK(0, mma16816_z) OSCAR_QK(1, mma16816) }
+      if (gq == 1) { OSCAR_QK(2, mma16816_z) OSCAR_QK(3, mma16816) }
+      if (gq == 2) { OSCAR_QK(4, mma16816_z) OSCAR_QK(5, mma16816) }
+      if (gq == 3) { OSCAR_QK(6, mma16816_z) OSCAR_QK(7, mma16816) }
     } else {
-      if (gq == 0) { OSCAR_QK(0, true) OSCAR_QK(1, false) OSCAR_QK(2, false) OSCAR_QK(3, false) }
-      if (gq == 1) { OSCAR_QK(4, true) OSCAR_QK(5, false) OSCAR_QK(6, false) OSCAR_QK(7, false) }
+      if (gq == 0) { OSCAR_QK(0, mma16816_z) OSCAR_QK(1, mma16816) OSCAR_QK(2, mma16816) OSCAR_QK(3, mma16816) }
+      if (gq == 1) { OSCAR_QK(4, mma16816_z) OSCAR_QK(5, mma16816) OSCAR_QK(6, mma16816) OSCAR_QK(7, mma16816) }
     }
 #undef OSCAR_QK
     const float2 se = h2_bits_to_f2(*reinterpret_cast<const uint32_t*>(s0 + 4 * gq));            // 2 tig, 2 tig + 8
     const float2 so = h2_bits_to_f2(*reinterpret_cast<const uint32_t*>(s0 + 4 * NG + 4 * gq));   // 2 tig + 1, + 9
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      u[mt][0][0] = fmaf(se.x, c[mt][0][0], u[mt][0][0]);
-      u[mt][0][1] = fmaf(so.x, c[mt][0][1], u[mt][0][1]);
-      u[mt][0][2] = fmaf(se.x, c[mt][0][2], u[mt][0][2]);
-      u[mt][0][3] = fmaf(so.x, c[mt][0][3], u[mt][0][3]);
-      u[mt][1][0] = fmaf(se.y, c[mt][1][0], u[mt][1][0]);
-      u[mt][1][1] = fmaf(so.y, c[mt][1][1], u[mt][1][1]);
-      u[mt][1][2] = fmaf(se.y, c[mt][1][2], u[mt][1][2]);
-      u[mt][1][3] = fmaf(so.y, c[mt][1][3], u[mt][1][3]);
-    }
+    u[0][0] = fmaf(se.x, c[0][0], u[0][0]);
+    u[0][1] = fmaf(so.x, c[0][1], u[0][1]);
+    u[0][2] = fmaf(se.x, c[0][2], u[0][2]);
+    u[0][3] = fmaf(so.x, c[0][3], u[0][3]);
+    u[1][0] = fmaf(se.y, c[1][0], u[1][0]);
+    u[1][1] = fmaf(so.y, c[1][1], u[1][1]);
+    u[1][2] = fmaf(se.y, c[1][2], u[1][2]);
+    u[1][3] = fmaf(so.y, c[1][3], u[1][3]);
   }
 }
 
-// running maxima and rescaling for NP pages' scores; us: score units per log2 unit
-template <int MT, int NP>
-__device__ __forceinline__ void update_max(State<MT>& st, const float (&u)[NP][MT][2][4], float us, float tau) {
-  float mx[MT][2];
+// running maxima and rescaling for a page's scores; us: score units per log2 unit
+__device__ __forceinline__ void update_max(State& st, const float (&u)[2][4], float us, float tau) {
+  float mx[2];
   bool over = false;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float x = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < NP; ++n)
-        x = fmaxf(x, fmaxf(fmaxf(u[n][mt][0][2 * r], u[n][mt][0][2 * r + 1]),
-                           fmaxf(u[n][mt][1][2 * r], u[n][mt][1][2 * r + 1])));
-      mx[mt][r] = x;
-      over |= x > st.m[mt][r] + tau;
-    }
+  for (int r = 0; r < 2; ++r) {
+    mx[r] = fmaxf(fmaxf(u[0][2 * r], u[0][2 * r + 1]), fmaxf(u[1][2 * r], u[1][2 * r + 1]));
+    over |= mx[r] > st.m[r] + tau;
+  }
   if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int r = 0; r < 2; ++r) {
+      const float x = quad_max(mx[r]);
+      const bool bump = x > st.m[r] + tau;
+      const float a = bump ? ex2((st.m[r] - x) * us) : 1.f;
+      st.m[r] = bump ? x : st.m[r];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float x = quad_max(mx[mt][r]);
-        const bool bump = x > st.m[mt][r] + tau;
-        const float a = bump ? ex2((st.m[mt][r] - x) * us) : 1.f;
-        st.m[mt][r] = bump ? x : st.m[mt][r];
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int xh = 0; xh < 2; ++xh) {
-            st.o[mt][i][xh][2 * r] *= a;
-            st.o[mt][i][xh][2 * r + 1] *= a;
-          }
-        st.oz[mt][2 * r] *= a;
-        st.oz[mt][2 * r + 1] *= a;
-      }
+        for (int xh = 0; xh < 2; ++xh) {
+          st.o[i][xh][2 * r] *= a;
+          st.o[i][xh][2 * r + 1] *= a;
+        }
+      st.oz[2 * r] *= a;
+      st.oz[2 * r + 1] *= a;
+    }
   }
 }
 
-// o += P V of one page; P: fp16 probabilities (times pscale) as row fragments
-template <int NG, int MT>
-__device__ __forceinline__ void page_values(const uint8_t* sb, int lane, const uint4 (&P)[MT], State<MT>& st) {
+// o += P V of one page; P: fp16 probabilities (times pscale) as a row fragment
+template <int NG>
+__device__ __forceinline__ void page_values(const uint8_t* sb, int lane, const uint4& P, State& st) {
   const int gid = lane >> 2, tig = lane & 3;
   const uint4 vw = *reinterpret_cast<const uint4*>(sb + 512 + lane * 16);
   const uint4 vh = shr10(vw);
@@ -336,20 +317,10 @@ __device__ __forceinline__ void page_values(const uint8_t* sb, int lane, const u
   for (int gq = 0; gq < NG; ++gq) {
     // scales of tokens (2 tig, 2 tig + 1) and (2 tig + 8, 2 tig + 9)
     const uint2 mv = *reinterpret_cast<const uint2*>(sb + vbase + 16 * (4 * gq + tig));
-    uint4 a[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      a[mt] = make_uint4(hmul2_bits(P[mt].x, mv.x), hmul2_bits(P[mt].y, mv.x), hmul2_bits(P[mt].z, mv.y),
-                         hmul2_bits(P[mt].w, mv.y));
-#define OSCAR_PV(I)                                                                    \
-  {                                                                                    \
-    const uint32_t x0 = slot_bits<I>(vw.x, vh.x), x1 = slot_bits<I>(vw.z, vh.z);       \
-    const uint32_t y0 = slot_bits<I>(vw.y, vh.y), y1 = slot_bits<I>(vw.w, vh.w);       \
-    _Pragma("unroll") for (int mt = 0; mt < MT; ++mt) {                                \
-      mma16816(st.o[mt][I][0], a[mt], x0, x1);                                         \
-      mma16816(st.o[mt][I][1], a[mt], y0, y1);                                         \
-    }                                                                                  \
-  }
+    const uint4 a = make_uint4(hmul2_bits(P.x, mv.x), hmul2_bits(P.y, mv.x), hmul2_bits(P.z, mv.y), hmul2_bits(P.w, mv.y));
+#define OSCAR_PV(I)                                                                     \
+  mma16816(st.o[I][0], a, slot_bits<I>(vw.x, vh.x), slot_bits<I>(vw.z, vh.z));          \
+  mma16816(st.o[I][1], a, slot_bits<I>(vw.y, vh.y), slot_bits<I>(vw.w, vh.w));
     if constexpr (NG == kGroups) {
       if (gq == 0) { OSCAR_PV(0) OSCAR_PV(1) }
       if (gq == 1) { OSCAR_PV(2) OSCAR_PV(3) }
@@ -366,58 +337,65 @@ __device__ __forceinline__ void page_values(const uint8_t* sb, int lane, const u
   constexpr uint32_t kOnes = 0x3c003c00u;
   uint2 mz = make_uint2(gid == 4 ? kOnes : 0u, gid == 4 ? kOnes : 0u);
   if (gid < NG) mz = *reinterpret_cast<const uint2*>(sb + vbase + 16 * (4 * gid + tig) + 8);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) mma16816(st.oz[mt], P[mt], mz.x, mz.y);
+  mma16816(st.oz, P, mz.x, mz.y);
 }
 
-// INT2 positions [lo, hi) of KV head h: slice `split` of `nsplits` of their pages
-template <int NG, int MT>
-__device__ void int2_part(const TreeParams& p, int b, int h, int tile, int split, int nsplits, int lo, int hi,
-                          uint8_t* smem, uint4* qs, State<MT>& st, float& unit, float& inv_ps) {
-  constexpr int NP = 1;   // pages per softmax step
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int first = lo / kPage;
-  const int npages = hi > lo ? (hi - 1) / kPage - first + 1 : 0;
-  const int chunk = (npages + nsplits - 1) / nsplits;
-  const int pbeg = first + split * chunk, pend = min(pbeg + chunk, first + npages);
-  // warp w takes pages pbeg + w + 8 j
-  const int nmine = pend - pbeg - warp > 0 ? (pend - pbeg - warp + kWarps - 1) / kWarps : 0;
-
-  // row tiles of 16 rows read half of a 32-row record
-  const uint32_t* rec = p.qrec + (((size_t)b * p.num_kv_heads + h) * p.row_tiles + tile * MT / 2) * kTreeRecWords;
-  const int mt0 = MT == 1 ? tile & 1 : 0;
-  for (int i = tid; i < MT * 8 * 32; i += kThreads) qs[i] = reinterpret_cast<const uint4*>(rec)[mt0 * 256 + i];
-  uint2 zs[MT];
+// fp16 probabilities (times 2^lg_ps) of a page's scores as a row fragment: half a step is
+// 2^-11 of a probability, and the denominator sums the rounded ones. Every row sees the
+// same tokens: a maximum of -inf means none so far
+__device__ __forceinline__ uint4 probabilities(const float (&u)[2][4], const float (&m)[2], float unit, float lg_ps) {
+  const float n0 = m[0] == -INFINITY ? 0.f : fmaf(-m[0], unit, lg_ps), n1 = m[1] == -INFINITY ? 0.f : fmaf(-m[1], unit, lg_ps);
+  float e[2][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) zs[mt] = *reinterpret_cast<const uint2*>(rec + kRecSums + 2 * ((mt0 + mt) * 32 + lane));
-  unit = __uint_as_float(rec[kRecUnit]);
-  const float tau = kLazyLog2 / unit;
-  const float pscale = p.pv_scale[h], lg_ps = log2f(pscale);
-  inv_ps = 1.f / pscale;
+  for (int th = 0; th < 2; ++th)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[th][i] = ex2(fmaf(u[th][i], unit, i < 2 ? n0 : n1));
+  return make_uint4(f2_to_h2_bits(e[0][0], e[0][1]), f2_to_h2_bits(e[0][2], e[0][3]), f2_to_h2_bits(e[1][0], e[1][1]),
+                    f2_to_h2_bits(e[1][2], e[1][3]));
+}
 
-  uint8_t* sbuf = smem + warp * kStages * kBlockBytes;
-  const uint32_t sring = (uint32_t)__cvta_generic_to_shared(sbuf) + lane * 16;
-  constexpr int kBB = block_bytes(NG);
-  const uint8_t* pool_h = p.pool + (size_t)h * kBB + lane * 16;
-  const size_t stride = (size_t)p.num_kv_heads * kBB;
-  const int32_t* row = p.page_table + (size_t)b * p.pt_stride;
-  // page ids of pages 32 n .. 32 n + 31 of this warp, one per lane, and the next 32
-  bool bad = false;
-  auto load_ids = [&](int j0) {
-    const int j = j0 + lane, at = pbeg + warp + kWarps * j;
+// the pages of one warp: ids, and copies into its ring slots. What the page loop does not
+// need stays in the kernel's parameters: registers are what limits the warps per SM
+template <int NG>
+struct PageStream {
+  const TreeParams& p;
+  int begin, nmine;        // the warp's first page, and how many it has: begin + 8 j
+  uint32_t off, sring;     // this lane's 16 bytes of a page's block of the head, and of ring slot 0
+  int ids, ids_next;       // pages 32 n .. + 31 of this warp, one per lane, and the next 32
+  uint32_t okbits;         // bit j % 32: page j of those in flight has a valid id
+
+  // slice `split` of `nsplits` of the pages of positions [lo, hi); warp w takes pages
+  // pbeg + w + 8 j. steps: the pages of the slice's warp `warp & ~1`
+  __device__ __forceinline__ PageStream(const TreeParams& params, int split, int nsplits, int lo, int hi, uint8_t* ring, int& steps)
+      : p(params) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = lo / kPage, npages = hi > lo ? (hi - 1) / kPage - first + 1 : 0;
+    const int chunk = (npages + nsplits - 1) / nsplits;
+    const int pbeg = first + split * chunk, n = min(chunk, first + npages - pbeg);
+    auto count = [&](int w) { return n > w ? (n - w + kWarps - 1) / kWarps : 0; };
+    begin = pbeg + warp;
+    nmine = count(warp);
+    steps = count(warp & ~1);
+    off = (uint32_t)blockIdx.y * block_bytes(NG) + lane * 16;
+    sring = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+    okbits = 0u;
+    ids = load_ids(0);
+    ids_next = load_ids(32);
+  }
+  __device__ __forceinline__ int load_ids(int j0) const {
+    const int j = j0 + (threadIdx.x & 31), at = begin + kWarps * j;
     int id = -1;
     if (j < nmine) {
-      id = at < p.pt_stride ? row[at] : -1;
+      id = at < p.pt_stride ? p.page_table[(size_t)blockIdx.z * p.pt_stride + at] : -1;
       if (id < 0 || id >= p.num_pages) {
-        bad = true;
+        atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
         id = -1;
       }
     }
     return id;
-  };
-  int ids = load_ids(0), ids_next = load_ids(32);
-  uint32_t okbits = 0u;   // bit j % 32: page j of those in flight has a valid id
-  auto issue = [&](int j) {
+  }
+  // page j into ring slot j % kStages (zeros for a page that is not there)
+  __device__ __forceinline__ void issue(int j) {
     if (j && (j & 31) == 0) {
       ids = ids_next;
       ids_next = load_ids(j + 32);
@@ -425,80 +403,69 @@ __device__ void int2_part(const TreeParams& p, int b, int h, int tile, int split
     const int id = j < nmine ? __shfl_sync(0xffffffffu, ids, j & 31) : -1;
     const uint32_t nb = id >= 0 ? 16u : 0u;
     okbits = (okbits & ~(1u << (j & 31))) | ((uint32_t)(id >= 0) << (j & 31));
-    const uint8_t* src = pool_h + (size_t)max(id, 0) * stride;
+    const uint8_t* src = p.pool + (uint64_t)(uint32_t)max(id, 0) * (uint32_t)(p.num_kv_heads * block_bytes(NG)) + off;
     const uint32_t dst = sring + (j & (kStages - 1)) * kBlockBytes;
     cp_async16(dst, src, nb);
     cp_async16(dst + 512, src + 512, nb);
-    if (NG == kGroups || lane < 16) cp_async16(dst + 1024, src + 1024, nb);
+    if (NG == kGroups || (threadIdx.x & 31) < 16) cp_async16(dst + 1024, src + 1024, nb);
     cp_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) issue(s);
-  __syncthreads();   // q~ fragments visible to every warp
+  }
+  // bits of page j's tokens that take part
+  __device__ __forceinline__ uint32_t valid(int j, int lo, int hi) const {
+    return page_token_bits((okbits >> (j & 31)) & 1u, (begin + kWarps * j) * kPage, lo, hi);
+  }
+};
 
-  for (int j = 0; j < nmine; j += NP) {
-    cp_wait<kStages - NP>();
+// INT2 positions [lo, hi) of KV head h: slice `split` of `nsplits` of their pages
+template <int NG>
+__device__ void int2_part(const TreeParams& p, int b, int h, int tile, int split, int nsplits, int lo, int hi,
+                          uint8_t* smem, uint4* qs, State& st, float& unit, float& inv_ps) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // row tiles of 16 rows read half of a 32-row record
+  const uint32_t* rec = p.qrec + (((size_t)b * p.num_kv_heads + h) * p.row_tiles + tile / 2) * kTreeRecWords;
+  const int mt = tile & 1;
+  for (int i = tid; i < 8 * 32; i += kThreads) qs[i] = reinterpret_cast<const uint4*>(rec)[mt * 256 + i];
+  const uint2 zs = *reinterpret_cast<const uint2*>(rec + kRecSums + 2 * (mt * 32 + lane));
+  unit = __uint_as_float(rec[kRecUnit]);
+  const float tau = kLazyLog2 / unit;
+  const float pscale = p.pv_scale[h], lg_ps = log2f(pscale);
+  inv_ps = 1.f / pscale;
+  uint8_t* ring = smem + warp * kStages * kBlockBytes;
+  int steps;
+  PageStream<NG> pages(p, split, nsplits, lo, hi, ring, steps);
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) pages.issue(s);
+  __syncthreads();   // q~ fragments visible to every warp
+  for (int j = 0; j < pages.nmine; ++j) {
+    cp_wait<kStages - 1>();
     __syncwarp();
-    float u[NP][MT][2][4];
-    uint8_t* sb[NP];
+    uint8_t* sb = ring + (j & (kStages - 1)) * kBlockBytes;
+    float u[2][4];
+    page_scores<NG>(sb, qs, zs, lane, u);
+    // tokens outside [lo, hi) or on a page whose id is outside the pool: scores -inf,
+    // value scales and zeros 0 in shared memory
+    const uint32_t valid = pages.valid(j, lo, hi);
+    if (valid != 0xffffu) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      sb[n] = sbuf + ((j + n) & (kStages - 1)) * kBlockBytes;
-      page_scores<NG, MT>(sb[n], qs, zs, lane, u[n]);
-    }
-    // tokens outside [lo, hi), on a page this warp does not have or whose id is
-    // outside the pool: scores -inf, value scales and zeros 0 in shared memory
-    uint32_t valid = 0u;
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-      valid |= page_token_bits((okbits >> ((j + n) & 31)) & 1u, (pbeg + warp + kWarps * (j + n)) * kPage, lo, hi) << (16 * n);
-    if (valid != (NP == 2 ? 0xffffffffu : 0xffffu)) {
-#pragma unroll
-      for (int n = 0; n < NP; ++n)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!((valid >> (16 * n + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1))) & 1u)) u[n][mt][i >> 2][i & 3] = -INFINITY;
-      zero_masked_value_meta<NG>(sb[0], sb[NP - 1], NP == 2 ? valid : valid | (valid << 16), lane);
+      for (int i = 0; i < 8; ++i)
+        if (!((valid >> (8 * (i >> 2) + 2 * (lane & 3) + (i & 1))) & 1u)) u[i >> 2][i & 3] = -INFINITY;
+      zero_masked_value_meta<NG>(sb, sb, valid | (valid << 16), lane);
       __syncwarp();
     }
-    update_max<MT, NP>(st, u, unit, tau);
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      uint4 P[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        // every row sees the same tokens: a maximum of -inf means none so far
-        const float n0 = st.m[mt][0] == -INFINITY ? 0.f : fmaf(-st.m[mt][0], unit, lg_ps);
-        const float n1 = st.m[mt][1] == -INFINITY ? 0.f : fmaf(-st.m[mt][1], unit, lg_ps);
-        float e[2][4];
-#pragma unroll
-        for (int th = 0; th < 2; ++th)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[th][i] = ex2(fmaf(u[n][mt][th][i], unit, i < 2 ? n0 : n1));
-        // rounded to fp16 for the tensor cores: half a step is 2^-12 of a
-        // probability, and the denominator sums the rounded ones
-        P[mt] = make_uint4(f2_to_h2_bits(e[0][0], e[0][1]), f2_to_h2_bits(e[0][2], e[0][3]),
-                           f2_to_h2_bits(e[1][0], e[1][1]), f2_to_h2_bits(e[1][2], e[1][3]));
-      }
-      page_values<NG, MT>(sb[n], lane, P, st);
-    }
+    update_max(st, u, unit, tau);
+    page_values<NG>(sb, lane, probabilities(u, st.m, unit, lg_ps), st);
     __syncwarp();
-#pragma unroll
-    for (int n = 0; n < NP; ++n) issue(j + n + kStages);
+    pages.issue(j + kStages);
   }
   cp_wait<0>();
-  if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
 }
 
 constexpr int kBfChunk = kTreeWindowChunk;   // tokens per BF16 CTA: one 16-token tile for each warp
-constexpr int kBfSmem(int mt) { return (2 * kBfChunk + 16 * mt) * kRow * 2; }
+constexpr int kBfSmem = (2 * kBfChunk + 16) * kRow * 2;
 
 // BF16 tokens [128 chunk, + 128) of the sink, the ring and the tree's own nodes, raw basis
-template <int MT>
 __device__ void bf16_part(const TreeParams& p, int b, int h, int tile, int chunk, const oscar_seq_state& seq, int len,
-                          uint8_t* smem, State<MT>& st) {
+                          uint8_t* smem, State& st) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int g = p.gqa, S = p.sink, W = p.recent;
   __shared__ unsigned long long anc[kTreeNodes];
@@ -529,8 +496,8 @@ __device__ void bf16_part(const TreeParams& p, int b, int h, int tile, int chunk
     cp_async16(sk + (r * kRow + 8 * u) * 2, ks, in ? 16u : 0u);
     cp_async16(sv + (r * kRow + 8 * u) * 2, vs, in ? 16u : 0u);
   }
-  const int ncol = len * g, col0 = tile * 16 * MT;
-  for (int i = tid; i < 16 * MT * 16; i += kThreads) {
+  const int ncol = len * g, col0 = tile * 16;
+  for (int i = tid; i < 16 * 16; i += kThreads) {
     const int r = i >> 4, u = i & 15, col = col0 + r, node = col / g, m = col - node * g;
     const bool in = col < ncol;
     const size_t off = in ? (((size_t)b * p.nodes + node) * p.num_q_heads + h * g + m) * kHeadDim + 8 * u : 0;
@@ -541,192 +508,120 @@ __device__ void bf16_part(const TreeParams& p, int b, int h, int tile, int chunk
   cp_wait<0>();
   __syncthreads();
   if (16 * warp >= n) return;   // no barrier below in this function
-  float u[1][MT][2][4] = {};
+  float u[2][4] = {};
   const uint32_t krow = sk + ((16 * warp + (lane & 7) + 8 * (lane >> 4)) * kRow + 8 * ((lane >> 3) & 1)) * 2;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     const uint4 kf = ldsm_x4(krow + 32 * kk);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const uint4 a = ldsm_x4(sq + ((16 * mt + (lane & 15)) * kRow + 16 * kk + 8 * (lane >> 4)) * 2);
-      mma16816_bf16(u[0][mt][0], a, kf.x, kf.y);
-      mma16816_bf16(u[0][mt][1], a, kf.z, kf.w);
-    }
+    const uint4 a = ldsm_x4(sq + ((lane & 15) * kRow + 16 * kk + 8 * (lane >> 4)) * 2);
+    mma16816_bf16(u[0], a, kf.x, kf.y);
+    mma16816_bf16(u[1], a, kf.z, kf.w);
   }
   const int tree0 = ns + nr - t0;   // row of node 0 in this chunk
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int node = min((col0 + 16 * mt + 8 * r + gid) / g, kTreeNodes - 1);
-      const unsigned long long sees = anc[node];
-#pragma unroll
-      for (int th = 0; th < 2; ++th)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int t = 16 * warp + 8 * th + 2 * tig + e, d = t - tree0;
-          const bool on = t < n && (d < 0 || ((sees >> d) & 1ull));
-          float& x = u[0][mt][th][2 * r + e];
-          x = on ? x * p.scale_log2 : -INFINITY;
-        }
-    }
-  update_max<MT, 1>(st, u, 1.f, 0.f);
-  // probabilities and values on the bf16 tensor cores, the probabilities split
-  // into two bf16 parts (16 bits), so that any bf16 value is exact
-  uint4 hi[MT], lo[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    uint32_t hw[4], lw[4];
-    float sum[2] = {0.f, 0.f};
+  for (int r = 0; r < 2; ++r) {
+    const unsigned long long sees = anc[min((col0 + 8 * r + gid) / g, kTreeNodes - 1)];
 #pragma unroll
     for (int th = 0; th < 2; ++th)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float nb = st.m[mt][r] == -INFINITY ? 0.f : -st.m[mt][r];
-        const float e0 = ex2(u[0][mt][th][2 * r] + nb), e1 = ex2(u[0][mt][th][2 * r + 1] + nb);
-        const uint32_t x = f2_to_bf2_bits(e0, e1);
-        const float2 xf = bf2_bits_to_f2(x);
-        const uint32_t y = f2_to_bf2_bits(e0 - xf.x, e1 - xf.y);
-        const float2 yf = bf2_bits_to_f2(y);
-        hw[2 * th + r] = x;
-        lw[2 * th + r] = y;
-        sum[r] += (xf.x + yf.x) + (xf.y + yf.y);
+      for (int e = 0; e < 2; ++e) {
+        const int t = 16 * warp + 8 * th + 2 * tig + e, d = t - tree0;
+        const bool on = t < n && (d < 0 || ((sees >> d) & 1ull));
+        float& x = u[th][2 * r + e];
+        x = on ? x * p.scale_log2 : -INFINITY;
       }
-    hi[mt] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-    lo[mt] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-    const float l0 = quad_sum(sum[0]), l1 = quad_sum(sum[1]);
-    st.oz[mt][0] = tig == 2 ? l0 : 0.f;   // column 4 is the denominator, no zero points
-    st.oz[mt][2] = tig == 2 ? l1 : 0.f;
   }
+  update_max(st, u, 1.f, 0.f);
+  // probabilities and values on the bf16 tensor cores, the probabilities split
+  // into two bf16 parts (16 bits), so that any bf16 value is exact
+  uint32_t hw[4], lw[4];
+  float sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int th = 0; th < 2; ++th)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float nb = st.m[r] == -INFINITY ? 0.f : -st.m[r];
+      const float e0 = ex2(u[th][2 * r] + nb), e1 = ex2(u[th][2 * r + 1] + nb);
+      const uint32_t x = f2_to_bf2_bits(e0, e1);
+      const float2 xf = bf2_bits_to_f2(x);
+      const uint32_t y = f2_to_bf2_bits(e0 - xf.x, e1 - xf.y);
+      const float2 yf = bf2_bits_to_f2(y);
+      hw[2 * th + r] = x;
+      lw[2 * th + r] = y;
+      sum[r] += (xf.x + yf.x) + (xf.y + yf.y);
+    }
+  const uint4 hi = make_uint4(hw[0], hw[1], hw[2], hw[3]), lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+  const float l0 = quad_sum(sum[0]), l1 = quad_sum(sum[1]);
+  st.oz[0] = tig == 2 ? l0 : 0.f;   // column 4 is the denominator, no zero points
+  st.oz[2] = tig == 2 ? l1 : 0.f;
   const uint32_t vrow = sv + ((16 * warp + (lane & 15)) * kRow + 8 * (lane >> 4)) * 2;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint4 vf = ldsm_x4_t(vrow + 32 * i);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      mma16816_bf16(st.o[mt][i][0], lo[mt], vf.x, vf.y);
-      mma16816_bf16(st.o[mt][i][1], lo[mt], vf.z, vf.w);
-      mma16816_bf16(st.o[mt][i][0], hi[mt], vf.x, vf.y);
-      mma16816_bf16(st.o[mt][i][1], hi[mt], vf.z, vf.w);
-    }
+    mma16816_bf16(st.o[i][0], lo, vf.x, vf.y);
+    mma16816_bf16(st.o[i][1], lo, vf.z, vf.w);
+    mma16816_bf16(st.o[i][0], hi, vf.x, vf.y);
+    mma16816_bf16(st.o[i][1], hi, vf.z, vf.w);
   }
 }
 
-constexpr int tree_smem(int mt) {
-  const int merge = (kWarps * 16 * mt * kPartRow + kWarps * 16 * mt * 3 + 16 * mt * 2) * 4;
-  const int int2 = kWarps * kStages * kBlockBytes + mt * 8 * 32 * 16;
-  const int bf = kBfSmem(mt);
-  return merge > int2 ? (merge > bf ? merge : bf) : (int2 > bf ? int2 : bf);
-}
+constexpr int kMaxOf(int a, int b) { return a > b ? a : b; }
+constexpr int kTreeSmem =
+    kMaxOf((kWarps * 16 * kPartRow + kWarps * 16 * 3) * 4, kMaxOf(kWarps * kStages * kBlockBytes + 8 * 32 * 16, kBfSmem));
 
-template <int NG, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) oscar_tree_attn_kernel(TreeParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
+// the 8 warps' partials to shared memory, then their merge into the call's partial rows
+template <int NG>
+__device__ void merge_warps(const State& st, float unit, float inv_ps, bool int2, uint8_t* smem, float* part, int col0, int ncol) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
-  const int ntiles = p.col_tiles, tile = blockIdx.x % ntiles, slot = blockIdx.x / ntiles;
-  const int h = blockIdx.y, b = blockIdx.z;
-  constexpr int NC = 16 * MT;
-  pdl_wait();
-  pdl_trigger();
-  const oscar_seq_state seq = p.state[b];
-  const int len = p.draft_len ? p.draft_len[b] : p.nodes;
-  const int ncol = len * p.gqa, col0 = tile * NC;
-  // a bad state or length: the merge writes the request's zeros and reads no partial
-  if (!state_ok(seq, p.sink, p.recent, p.max_batch) || len < 0 || len > p.nodes || col0 >= ncol) return;
-  State<MT> st;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    st.m[mt][0] = st.m[mt][1] = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st.oz[mt][i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) st.o[mt][i][j >> 2][j & 3] = 0.f;
-  }
-  const int nslots = p.win_slots + p.splits;
-  const int rows = p.nodes * p.gqa;
-  float* part = p.part + (((size_t)b * p.num_kv_heads + h) * nslots + slot) * rows * (size_t)kPartFloats;
-  float unit = 1.f, inv_ps = 1.f;
-  const bool int2 = slot >= p.win_slots;
-  const int lo = p.sink, hi = min(seq.int2_end, seq.seq_len);
-  bool empty;
-  if (int2) {
-    const int npages = hi > lo ? (hi - 1) / kPage - lo / kPage + 1 : 0;
-    empty = (slot - p.win_slots) * ((npages + p.splits - 1) / p.splits) >= npages;
-  } else {
-    const int rb = max(seq.int2_end, p.sink);
-    empty = slot * kBfChunk >= min(p.sink, seq.seq_len) + max(seq.seq_len - rb, 0) + len;
-  }
-  if (empty) {   // no keys: the merge skips the slot
-    for (int i = tid; i < min(NC, ncol - col0); i += kThreads) {
-      part[(size_t)(col0 + i) * kPartFloats + kHeadDim] = -INFINITY;
-      part[(size_t)(col0 + i) * kPartFloats + kHeadDim + 1] = 0.f;
-    }
-    return;
-  }
-  if (int2)
-    int2_part<NG, MT>(p, b, h, tile, slot - p.win_slots, p.splits, lo, hi, smem,
-                      reinterpret_cast<uint4*>(smem + kWarps * kStages * kBlockBytes), st, unit, inv_ps);
-  else
-    bf16_part<MT>(p, b, h, tile, slot, seq, len, smem, st);
-
-  // ---- the 8 warps' partials -> shared memory, then the CTA's merge -----------
   __syncthreads();   // staging buffers are reused
-  float* wpart = reinterpret_cast<float*>(smem);            // [8 warps][NC][kPartRow]
-  float* wml = wpart + kWarps * NC * kPartRow;              // [8 warps][NC][2]
-  float* wts = wml + kWarps * NC * 2;                       // [NC][8]
+  float* wpart = reinterpret_cast<float*>(smem);            // [8 warps][16][kPartRow]
+  float* wml = wpart + kWarps * 16 * kPartRow;              // [8 warps][16][2]
+  float* wts = wml + kWarps * 16 * 2;                       // [16][8]
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int i = 0; i < 8; ++i) {
+    // zero-point sums of channel block i's group: lane tig = group / 2, element group % 2
+    const int gq = i / (8 / NG), src = (lane & ~3) | (gq >> 1);
+    const float z0 = __shfl_sync(0xffffffffu, st.oz[gq & 1], src) * inv_ps;
+    const float z1 = __shfl_sync(0xffffffffu, st.oz[2 + (gq & 1)], src) * inv_ps;
+    const float sc = int2 ? 16777216.f / slot_factor(i) * inv_ps : 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // zero-point sums of channel block i's group: lane tig = group / 2, element group % 2
-      const int gq = i / (8 / NG), src = (lane & ~3) | (gq >> 1);
-      const float z0 = __shfl_sync(0xffffffffu, st.oz[mt][gq & 1], src) * inv_ps;
-      const float z1 = __shfl_sync(0xffffffffu, st.oz[mt][2 + (gq & 1)], src) * inv_ps;
-      const float sc = int2 ? 16777216.f / slot_factor(i) * inv_ps : 1.f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float* dst = wpart + (warp * NC + 16 * mt + gid) * kPartRow + 16 * i + 8 * x + 2 * tig;
-        const float* a = st.o[mt][i][x];
-        *reinterpret_cast<float2*>(dst) = make_float2(fmaf(a[0], sc, z0), fmaf(a[1], sc, z0));
-        *reinterpret_cast<float2*>(dst + 8 * kPartRow) = make_float2(fmaf(a[2], sc, z1), fmaf(a[3], sc, z1));
-      }
+    for (int x = 0; x < 2; ++x) {
+      float* dst = wpart + (warp * 16 + gid) * kPartRow + 16 * i + 8 * x + 2 * tig;
+      const float* a = st.o[i][x];
+      *reinterpret_cast<float2*>(dst) = make_float2(fmaf(a[0], sc, z0), fmaf(a[1], sc, z0));
+      *reinterpret_cast<float2*>(dst + 8 * kPartRow) = make_float2(fmaf(a[2], sc, z1), fmaf(a[3], sc, z1));
     }
-    if (tig == 2) {
-      float* d0 = wml + (warp * NC + 16 * mt + gid) * 2;
-      d0[0] = st.m[mt][0] * unit;
-      d0[1] = st.oz[mt][0] * inv_ps;
-      d0[16] = st.m[mt][1] * unit;
-      d0[17] = st.oz[mt][2] * inv_ps;
-    }
+  }
+  if (tig == 2) {
+    float* d = wml + (warp * 16 + gid) * 2;
+    d[0] = st.m[0] * unit;
+    d[1] = st.oz[0] * inv_ps;
+    d[16] = st.m[1] * unit;
+    d[17] = st.oz[2] * inv_ps;
   }
   __syncthreads();
-  if (tid < NC * kWarps) {   // thread (row n, warp w): the 8 warps of a row are consecutive lanes
+  if (tid < 16 * kWarps) {   // thread (row n, warp w): the 8 warps of a row are consecutive lanes
     const int n = tid >> 3, w = tid & 7;
-    const float mw = wml[(w * NC + n) * 2];
+    const float mw = wml[(w * 16 + n) * 2];
     float M = mw;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float sw = mw == -INFINITY ? 0.f : exp2f(mw - M);
-    float l = sw * wml[(w * NC + n) * 2 + 1];
+    float l = sw * wml[(w * 16 + n) * 2 + 1];
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     wts[n * kWarps + w] = sw;
-    if (w == 0 && col0 + n < ncol) {
-      float* dst = part + (size_t)(col0 + n) * kPartFloats + kHeadDim;
-      dst[0] = M;
-      dst[1] = l;
-    }
+    if (w == 0 && col0 + n < ncol)
+      *reinterpret_cast<float2*>(part + (size_t)(col0 + n) * kPartFloats + kHeadDim) = make_float2(M, l);
   }
   __syncthreads();
-  for (int i = tid; i < min(NC, ncol - col0) * 32; i += kThreads) {
+  for (int i = tid; i < min(16, ncol - col0) * 32; i += kThreads) {
     const int n = i >> 5, c = 4 * (i & 31);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float a = wts[n * kWarps + w];
-      const float4 x = *reinterpret_cast<const float4*>(wpart + (w * NC + n) * kPartRow + c);
+      const float4 x = *reinterpret_cast<const float4*>(wpart + (w * 16 + n) * kPartRow + c);
       o.x = fmaf(a, x.x, o.x);
       o.y = fmaf(a, x.y, o.y);
       o.z = fmaf(a, x.z, o.z);
@@ -736,20 +631,413 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) oscar_tree_attn_ker
   }
 }
 
+// A CTA's share of a request: the state, its rows and whether its slot has keys. False: no
+// rows here, or a bad state or length (the merge then writes the request's zeros and reads
+// no partial), or no keys (rows col0 .. col0 + nc - 1 of the slot are marked empty).
+struct Slot {
+  oscar_seq_state seq;
+  int len, ncol, lo, hi;
+  float* part;   // the slot's partial rows
+};
+__device__ __forceinline__ bool open_slot(const TreeParams& p, int b, int h, int slot, int col0, int nc, Slot& s) {
+  s.seq = p.state[b];
+  s.len = p.draft_len ? p.draft_len[b] : p.nodes;
+  s.ncol = s.len * p.gqa;
+  if (!state_ok(s.seq, p.sink, p.recent, p.max_batch) || s.len < 0 || s.len > p.nodes || col0 >= s.ncol) return false;
+  const int nslots = p.win_slots + p.splits, rows = p.nodes * p.gqa;
+  s.part = p.part + (((size_t)b * p.num_kv_heads + h) * nslots + slot) * rows * (size_t)kPartFloats;
+  s.lo = p.sink;
+  s.hi = min(s.seq.int2_end, s.seq.seq_len);
+  bool empty;
+  if (slot >= p.win_slots) {
+    const int npages = s.hi > s.lo ? (s.hi - 1) / kPage - s.lo / kPage + 1 : 0;
+    empty = (slot - p.win_slots) * ((npages + p.splits - 1) / p.splits) >= npages;
+  } else {
+    const int rb = max(s.seq.int2_end, p.sink);
+    empty = slot * kBfChunk >= min(p.sink, s.seq.seq_len) + max(s.seq.seq_len - rb, 0) + s.len;
+  }
+  if (empty)
+    for (int i = threadIdx.x; i < min(nc, s.ncol - col0); i += kThreads)
+      *reinterpret_cast<float2*>(s.part + (size_t)(col0 + i) * kPartFloats + kHeadDim) = make_float2(-INFINITY, 0.f);
+  return !empty;
+}
+
+// a tile of 16 rows over the BF16 tokens or the split of a slot
+template <int NG>
+__device__ __forceinline__ void small_tile(const TreeParams& p, int b, int h, int tile, int slot, const Slot& s, uint8_t* smem) {
+  State st;
+  st.clear();
+  float unit = 1.f, inv_ps = 1.f;
+  const bool int2 = slot >= p.win_slots;
+  if (int2)
+    int2_part<NG>(p, b, h, tile, slot - p.win_slots, p.splits, s.lo, s.hi, smem,
+                  reinterpret_cast<uint4*>(smem + kWarps * kStages * kBlockBytes), st, unit, inv_ps);
+  else
+    bf16_part(p, b, h, tile, slot, s.seq, s.len, smem, st);
+  merge_warps<NG>(st, unit, inv_ps, int2, smem, s.part, 16 * tile, s.ncol);
+}
+
+template <int NG>
+__global__ void __launch_bounds__(kThreads, 2) oscar_tree_attn_kernel(TreeParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tile = blockIdx.x % p.col_tiles, slot = blockIdx.x / p.col_tiles, h = blockIdx.y, b = blockIdx.z;
+  pdl_wait();
+  pdl_trigger();
+  Slot s;
+  if (open_slot(p, b, h, slot, 16 * tile, 16, s)) small_tile<NG>(p, b, h, tile, slot, s, smem);
+}
+
 // --------------------------------------------------------------------------
-// 3. merge: CTA x handles 16 query rows of (request z, KV head y)
+// 2b. the same for 17 .. 32 query rows: two warps share a page pair. Each scores its own
+//     page for all 32 rows and hands its probabilities to the other; each adds both
+//     pages' values for its half of the channels. A warp then holds 64 value sums per
+//     lane instead of 128, so four warps fit a scheduler instead of two (the 128-register
+//     layout above is bound by the latency of its two warps: 41 % issue, 48 % tensor).
+//     The scores take dequantised keys (s c 2^m, 3 s rounded to fp16; the zero points
+//     enter as above), which saves the group sums' scaling.
+// --------------------------------------------------------------------------
+constexpr int kPairs = kWarps / 2;
+struct PairSmem {
+  uint8_t ring[kWarps][kStages][kBlockBytes];
+  uint4 q[2 * 8 * 32];
+  uint4 P[kWarps][2][32];
+  float mx[kWarps][32];
+  // read again at each page: they would not fit the registers
+  uint2 zs[2][32];
+  float unit, tau, lg_ps;
+  uint32_t mul, zmul;
+};
+struct PairOut {   // over the same memory, after the last page
+  float o[kPairs][32][kPartRow];
+  float z[kWarps][32][8];          // group zero sums, [4] the denominator
+  float m[kPairs][32];
+  float w[32][kPairs];
+};
+constexpr int kPairSmem = kMaxOf(kMaxOf((int)sizeof(PairOut), (int)sizeof(PairSmem)), kTreeSmem);
+
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + pair) : "memory"); }
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r) : "r"((uint32_t)x), "r"(1 + pair) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t half2_of(float x) {
+  const __half2 r = __float2half2_rn(x);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// scores of one page against dequantised keys: u[mt][th] as in page_scores
+template <int NG>
+__device__ __forceinline__ void page_scores_deq(const uint8_t* sb, const uint4* qs, const uint2 (&zs)[2][32], int lane, uint32_t mul,
+                                                uint32_t zmul, float (&u)[2][2][4]) {
+  const int gid = lane >> 2, tig = lane & 3;
+  const uint4 kw = *reinterpret_cast<const uint4*>(sb + lane * 16);
+  const uint4 kh = shr10(kw);
+  {
+    const int zo = kzero_off(NG, gid, NG == kGroups ? 2 * (tig & 1) : 0);
+    constexpr int step = kzero_off(NG, 8, 0) - kzero_off(NG, 0, 0);
+    const bool on = NG == kGroups || tig < 2;
+    const uint32_t z0 = on ? hmul2_bits(*reinterpret_cast<const uint32_t*>(sb + zo), zmul) : 0u;
+    const uint32_t z1 = on ? hmul2_bits(*reinterpret_cast<const uint32_t*>(sb + zo + step), zmul) : 0u;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint2 a = zs[mt][lane];
+      mma1688_z(u[mt][0], a, z0);
+      mma1688_z(u[mt][1], a, z1);
+    }
+  }
+  uint32_t s0 = 0u, s1 = 0u;   // a group's scales of tokens gid and gid + 8, in both halves
+#define OSCAR_QK(I)                                                                                       \
+  {                                                                                                       \
+    if constexpr ((I) % (8 / NG) == 0) {                                                                  \
+      const uint32_t w = hmul2_bits(*reinterpret_cast<const uint32_t*>(sb + kscale_off(NG, gid, (I) / (8 / NG))), mul); \
+      s0 = __byte_perm(w, w, 0x1010);                                                                     \
+      s1 = __byte_perm(w, w, 0x3232);                                                                     \
+    }                                                                                                     \
+    const uint32_t x0 = hmul2_bits(slot_bits<I>(kw.x, kh.x), s0), x1 = hmul2_bits(slot_bits<I>(kw.y, kh.y), s0); \
+    const uint32_t y0 = hmul2_bits(slot_bits<I>(kw.z, kh.z), s1), y1 = hmul2_bits(slot_bits<I>(kw.w, kh.w), s1); \
+    _Pragma("unroll") for (int mt = 0; mt < 2; ++mt) {                                                    \
+      const uint4 a = qs[(mt * 8 + (I)) * 32 + lane];                                                     \
+      mma16816(u[mt][0], a, x0, x1);                                                                      \
+      mma16816(u[mt][1], a, y0, y1);                                                                      \
+    }                                                                                                     \
+  }
+  OSCAR_QK(0) OSCAR_QK(1) OSCAR_QK(2) OSCAR_QK(3) OSCAR_QK(4) OSCAR_QK(5) OSCAR_QK(6) OSCAR_QK(7)
+#undef OSCAR_QK
+}
+
+// half of the channels (slots 4 half .. + 3) of one page's values: o += P V
+template <int NG>
+__device__ __forceinline__ void page_values_half(const uint8_t* sb, int lane, int half, const uint4 (&P)[2], float (&o)[2][4][2][4]) {
+  const int tig = lane & 3;
+  uint4 w = *reinterpret_cast<const uint4*>(sb + 512 + lane * 16);
+  // slots 4 half + i at bits 2 i of each half word
+  w.x >>= 8 * half;
+  w.y >>= 8 * half;
+  w.z >>= 8 * half;
+  w.w >>= 8 * half;
+  uint4 a[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i % (8 / NG) == 0) {
+      const int gq = (4 * half + i) / (8 / NG);
+      const uint2 mv = *reinterpret_cast<const uint2*>(sb + vscale_off(NG, 0, 0) + 16 * (4 * gq + tig));
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+        a[mt] = make_uint4(hmul2_bits(P[mt].x, mv.x), hmul2_bits(P[mt].y, mv.x), hmul2_bits(P[mt].z, mv.y),
+                           hmul2_bits(P[mt].w, mv.y));
+    }
+    const uint32_t bits = 0x00030003u << (2 * i);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      mma16816(o[mt][i][0], a[mt], w.x & bits, w.z & bits);
+      mma16816(o[mt][i][1], a[mt], w.y & bits, w.w & bits);
+    }
+  }
+}
+
+template <int NG>
+__device__ void int2_pair(const TreeParams& p, int b, int h, int split, int nsplits, int lo, int hi, uint8_t* smem, float* part,
+                          int ncol) {
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3, pair = warp >> 1, half = warp & 1;
+  const uint32_t* rec = p.qrec + ((size_t)b * p.num_kv_heads + h) * p.row_tiles * kTreeRecWords;
+  for (int i = tid; i < 2 * 8 * 32; i += kThreads) sm.q[i] = reinterpret_cast<const uint4*>(rec)[i];
+  if (tid < 64) {   // the group sums carry 2^-24: to 2^-9, since z 2^m does not fit fp16
+    const uint2 z = *reinterpret_cast<const uint2*>(rec + kRecSums + 2 * tid);
+    const uint32_t up = half2_of(32768.f);
+    sm.zs[tid >> 5][lane] = make_uint2(hmul2_bits(z.x, up), hmul2_bits(z.y, up));
+  }
+  if (tid == 0) {
+    const int mk = scale_exponent(p.clip_K[h]);
+    sm.mul = half2_of(ldexpf(1.f, mk));
+    sm.zmul = half2_of(ldexpf(1.f, mk - 15));
+    sm.unit = __uint_as_float(rec[kRecUnit]) * ldexpf(1.f, -mk);
+    sm.tau = kLazyLog2 / sm.unit;
+    sm.lg_ps = log2f(p.pv_scale[h]);
+  }
+  const int first = lo / kPage;
+  const int npages = hi > lo ? (hi - 1) / kPage - first + 1 : 0;
+  const int chunk = (npages + nsplits - 1) / nsplits;
+  const int pbeg = first + split * chunk, pend = min(pbeg + chunk, first + npages);
+  // warp w takes pages pbeg + w + 8 j; both warps of a pair take the even one's steps
+  auto count = [&](int w) { return pend - pbeg - w > 0 ? (pend - pbeg - w + kWarps - 1) / kWarps : 0; };
+  const int nmine = count(warp), steps = count(warp & ~1);
+  const uint32_t sring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0]) + lane * 16;
+  constexpr int kBB = block_bytes(NG);
+  auto load_ids = [&](int j0) {   // pages 32 n .. + 31 of this warp, one per lane
+    const int j = j0 + lane, at = pbeg + warp + kWarps * j;
+    int id = -1;
+    if (j < nmine) {
+      id = at < p.pt_stride ? p.page_table[(size_t)b * p.pt_stride + at] : -1;
+      if (id < 0 || id >= p.num_pages) {
+        atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
+        id = -1;
+      }
+    }
+    return id;
+  };
+  int ids = load_ids(0), ids_next = load_ids(32);
+  uint32_t okbits = 0u;
+  auto issue = [&](int j) {
+    if (j && (j & 31) == 0) {
+      ids = ids_next;
+      ids_next = load_ids(j + 32);
+    }
+    const int id = j < nmine ? __shfl_sync(0xffffffffu, ids, j & 31) : -1;
+    const uint32_t nb = id >= 0 ? 16u : 0u;
+    okbits = (okbits & ~(1u << (j & 31))) | ((uint32_t)(id >= 0) << (j & 31));
+    const uint8_t* src = p.pool + (uint64_t)(uint32_t)max(id, 0) * (uint32_t)(p.num_kv_heads * kBB) + (uint32_t)(h * kBB + lane * 16);
+    const uint32_t dst = sring + (j & (kStages - 1)) * kBlockBytes;
+    cp_async16(dst, src, nb);
+    cp_async16(dst + 512, src + 512, nb);
+    if (NG == kGroups || lane < 16) cp_async16(dst + 1024, src + 1024, nb);
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
+  __syncthreads();   // q~ fragments visible to every warp
+
+  float o[2][4][2][4], oz[2][4], m[2][2];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    m[mt][0] = m[mt][1] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      oz[mt][i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[mt][i][e >> 2][e & 3] = 0.f;
+    }
+  }
+  for (int j = 0; j < steps; ++j) {
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    uint8_t* sb = sm.ring[warp][j & (kStages - 1)];
+    float u[2][2][4];
+    page_scores_deq<NG>(sb, sm.q, sm.zs, lane, sm.mul, sm.zmul, u);
+    const float unit = sm.unit, tau = sm.tau;
+    const uint32_t valid = page_token_bits((okbits >> (j & 31)) & 1u, (pbeg + warp + kWarps * j) * kPage, lo, hi);
+    if (valid != 0xffffu) {   // scores -inf, value scales and zeros 0 in shared memory
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!((valid >> (8 * (i >> 2) + 2 * tig + (i & 1))) & 1u)) u[mt][i >> 2][i & 3] = -INFINITY;
+      zero_masked_value_meta<NG>(sb, sb, valid | (valid << 16), lane);
+    }
+    float mx[2][2];
+    bool over = false;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[mt][r] = fmaxf(fmaxf(u[mt][0][2 * r], u[mt][0][2 * r + 1]), fmaxf(u[mt][1][2 * r], u[mt][1][2 * r + 1]));
+        over |= mx[mt][r] > m[mt][r] + tau;
+      }
+    // the pair's vote; past it the other warp is done with the page before this one, whose
+    // slot is refilled
+    const bool move = pair_any(pair, over);
+    issue(j + kStages - 1);
+    if (move) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          mx[mt][r] = quad_max(mx[mt][r]);
+          if (tig == 0) sm.mx[warp][16 * mt + 8 * r + gid] = mx[mt][r];
+        }
+      pair_sync(pair);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float x = fmaxf(mx[mt][r], sm.mx[warp ^ 1][16 * mt + 8 * r + gid]);
+          const bool bump = x > m[mt][r] + tau;
+          const float a = bump ? ex2((m[mt][r] - x) * unit) : 1.f;
+          m[mt][r] = bump ? x : m[mt][r];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int xh = 0; xh < 2; ++xh) {
+              o[mt][i][xh][2 * r] *= a;
+              o[mt][i][xh][2 * r + 1] *= a;
+            }
+          oz[mt][2 * r] *= a;
+          oz[mt][2 * r + 1] *= a;
+        }
+    }
+    uint4 P[2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      P[mt] = probabilities(u[mt], m[mt], unit, sm.lg_ps);
+      sm.P[warp][mt][lane] = P[mt];
+    }
+    pair_sync(pair);
+    // own page: also the zero-point sums and the denominator (column 4)
+    {
+      constexpr uint32_t kOnes = 0x3c003c00u;
+      uint2 mz = make_uint2(gid == 4 ? kOnes : 0u, gid == 4 ? kOnes : 0u);
+      if (gid < NG) mz = *reinterpret_cast<const uint2*>(sb + vscale_off(NG, 0, 0) + 16 * (4 * gid + tig) + 8);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) mma16816(oz[mt], P[mt], mz.x, mz.y);
+    }
+    page_values_half<NG>(sb, lane, half, P, o);
+    uint4 Q[2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) Q[mt] = sm.P[warp ^ 1][mt][lane];
+    page_values_half<NG>(sm.ring[warp ^ 1][j & (kStages - 1)], lane, half, Q, o);
+  }
+  cp_wait<0>();
+  const float unit = sm.unit, inv_ps = 1.f / p.pv_scale[h];
+
+  // ---- partials of the pairs -> shared memory, then their merge ------------------
+  __syncthreads();
+  PairOut& out = *reinterpret_cast<PairOut*>(smem);
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float sc = 16777216.f / (float)(1 << (2 * i)) * inv_ps;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float* dst = &out.o[pair][16 * mt + gid][16 * (4 * half + i) + 8 * x + 2 * tig];
+        const float* a = o[mt][i][x];
+        *reinterpret_cast<float2*>(dst) = make_float2(a[0] * sc, a[1] * sc);
+        *reinterpret_cast<float2*>(dst + 8 * kPartRow) = make_float2(a[2] * sc, a[3] * sc);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int rw = 16 * mt + 8 * r + gid;
+      *reinterpret_cast<float2*>(&out.z[warp][rw][2 * tig]) = make_float2(oz[mt][2 * r] * inv_ps, oz[mt][2 * r + 1] * inv_ps);
+      if (half == 0 && tig == 0) out.m[pair][rw] = m[mt][r] * unit;
+    }
+  }
+  __syncthreads();
+  if (tid < 32 * kPairs) {   // thread (row, pair): the pairs of a row are consecutive lanes
+    const int n = tid >> 2, w = tid & 3;
+    const float mw = out.m[w][n], M = quad_max(mw);
+    const float sw = mw == -INFINITY ? 0.f : exp2f(mw - M);
+    const float l = quad_sum(sw * (out.z[2 * w][n][4] + out.z[2 * w + 1][n][4]));
+    out.w[n][w] = sw;
+    if (w == 0 && n < ncol) *reinterpret_cast<float2*>(part + (size_t)n * kPartFloats + kHeadDim) = make_float2(M, l);
+  }
+  __syncthreads();
+  for (int i = tid; i < min(32, ncol) * 32; i += kThreads) {
+    const int n = i >> 5, c = 4 * (i & 31), gq = c / (kHeadDim / NG);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kPairs; ++w) {
+      const float a = out.w[n][w], z = out.z[2 * w][n][gq] + out.z[2 * w + 1][n][gq];
+      const float4 y = *reinterpret_cast<const float4*>(&out.o[w][n][c]);
+      x.x = fmaf(a, y.x + z, x.x);
+      x.y = fmaf(a, y.y + z, x.y);
+      x.z = fmaf(a, y.z + z, x.z);
+      x.w = fmaf(a, y.w + z, x.w);
+    }
+    *reinterpret_cast<float4*>(part + (size_t)n * kPartFloats + c) = x;
+  }
+}
+
+// grid x: two 16-row tiles of each BF16 chunk, then the splits
+template <int NG>
+__global__ void __launch_bounds__(kThreads, 2) oscar_tree_pair_kernel(TreeParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int h = blockIdx.y, b = blockIdx.z, x = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const bool int2 = x >= 2 * p.win_slots;
+  const int slot = int2 ? x - p.win_slots : x >> 1, tile = int2 ? 0 : x & 1;
+  Slot s;
+  if (!open_slot(p, b, h, slot, 16 * tile, int2 ? 32 : 16, s)) return;
+  if (int2 && s.ncol > 16)
+    int2_pair<NG>(p, b, h, slot - p.win_slots, p.splits, s.lo, s.hi, smem, s.part, s.ncol);
+  else   // BF16 tokens, or a request that uses few of its rows
+    small_tile<NG>(p, b, h, tile, slot, s, smem);
+}
+
+// --------------------------------------------------------------------------
+// 3. merge: CTA x handles R query rows of (request z, KV head y): 16, the height of the
+//    un-rotation's product, or 4 when those would be few CTAs (the merge is then a chain
+//    of load latencies, and a quarter of the rows is four times the loads in flight)
 // --------------------------------------------------------------------------
 constexpr int kMergeThreads = 128;
 constexpr int kMergeRows = 16;
+constexpr int kMergeFewRows = 4096;   // rows of a call up to which the merge takes 4 rows a CTA
 
+template <int R>
 __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreeParams p) {
+  constexpr int kPer = kMergeThreads / R;       // threads of a row
+  constexpr int kVec = kHeadDim / 4 / kPer;     // float4 pieces of each
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z, row0 = blockIdx.x * kMergeRows, g = p.gqa;
+  const int h = blockIdx.y, b = blockIdx.z, row0 = blockIdx.x * R, g = p.gqa;
   const int nslots = p.win_slots + p.splits, rows = p.nodes * g;
-  float* wts = reinterpret_cast<float*>(smem);            // [nslots][16]
+  float* wts = reinterpret_cast<float*>(smem);            // [nslots][R]
   __shared__ __align__(16) __half ox[kMergeRows][kRow];   // INT2 sums over the denominator (R_V basis)
-  __shared__ __align__(16) float ow[kMergeRows][kHeadDim + 4];   // window and tree sums over it
+  __shared__ __align__(16) float ow[R][kHeadDim + 4];   // window and tree sums over it
   // un-rotation operand, constant: warp w produces channels 32 w .. 32 w + 31,
   // out[n] = sum_k x[k] R_V[n][k]
   uint2 bf[4][8];
@@ -778,70 +1066,80 @@ __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreePar
   if (!tree_ok || !seq_ok) {
     if (tid == 0 && blockIdx.x == 0 && h == 0)
       atomicOr(p.err_flags, (tree_ok ? 0u : OSCAR_FLAG_BAD_TREE) | (seq_ok ? 0u : OSCAR_FLAG_BAD_STATE));
-    for (int i = tid; i < min(kMergeRows, rows - row0) * kHeadDim; i += kMergeThreads) {
+    for (int i = tid; i < min(R, rows - row0) * kHeadDim; i += kMergeThreads) {
       const int r = row0 + i / kHeadDim, node = r / g;
       p.o[(((size_t)b * p.nodes + node) * p.num_q_heads + h * g + (r - node * g)) * kHeadDim + i % kHeadDim] =
           __float2bfloat16(0.f);
     }
     return;
   }
-  const int nrows = min(kMergeRows, len * g - row0);
+  const int nrows = min(R, len * g - row0);
   if (nrows <= 0) return;   // rows of nodes the request does not use: left as they are
   const float* part = p.part + (((size_t)b * p.num_kv_heads + h) * nslots * rows + row0) * kPartFloats;
   const size_t slot_stride = (size_t)rows * kPartFloats;
-  // thread (row r, eighth j): slot weights over the denominator
-  const int r = tid >> 3, j = tid & 7;
+  // thread j of row r: slot weights over the denominator
+  const int r = tid / kPer, j = tid % kPer;
   float inv = 0.f;
   {
     float M = -INFINITY;
     if (r < nrows)
-      for (int s = j; s < nslots; s += 8) M = fmaxf(M, part[s * slot_stride + r * kPartFloats + kHeadDim]);
+      for (int s = j; s < nslots; s += kPer) M = fmaxf(M, part[s * slot_stride + r * kPartFloats + kHeadDim]);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 1; o < kPer; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float l = 0.f;
-    for (int s = j; s < nslots; s += 8) {
+    for (int s = j; s < nslots; s += kPer) {
       const float2 ml = r < nrows ? *reinterpret_cast<const float2*>(part + s * slot_stride + r * kPartFloats + kHeadDim)
                                   : make_float2(-INFINITY, 0.f);
       const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      wts[s * kMergeRows + r] = w;
+      wts[s * R + r] = w;
       l = fmaf(w, ml.y, l);
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = 1; o < kPer; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     inv = 1.f / l;   // a row always sees itself: l >= 1 up to rounding
   }
   __syncwarp();
-  float a2[16] = {}, aw[16] = {};
-  for (int s = 0; s < nslots; ++s) {
-    const float w = wts[s * kMergeRows + r];
-    if (w != 0.f) {   // a slot without keys left its sums unwritten
-      const float* src = part + s * slot_stride + r * kPartFloats + 4 * j;
-      const bool win = s < p.win_slots;
+  float a2[4 * kVec] = {}, aw[4 * kVec] = {};
+  const float* src = part + r * kPartFloats + 4 * j;
+  auto add = [&](float* a, int s0, int s1) {   // weighted sums of slots s0 .. s1 - 1
+    for (int s = s0; s < s1; s += 4) {
+      float4 x[4][kVec];
+      float w[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(src + 32 * c);
-        float* a = win ? aw + 4 * c : a2 + 4 * c;
-        a[0] = fmaf(w, x.x, a[0]);
-        a[1] = fmaf(w, x.y, a[1]);
-        a[2] = fmaf(w, x.z, a[2]);
-        a[3] = fmaf(w, x.w, a[3]);
+      for (int u = 0; u < 4; ++u) {   // a slot without keys left its sums unwritten
+        w[u] = s + u < s1 ? wts[(s + u) * R + r] : 0.f;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+          if (w[u] != 0.f) x[u][c] = *reinterpret_cast<const float4*>(src + (s + u) * slot_stride + 4 * kPer * c);
       }
-    }
-  }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    *reinterpret_cast<float4*>(&ow[r][32 * c + 4 * j]) =
+      for (int u = 0; u < 4; ++u)
+        if (w[u] != 0.f)
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) {
+            a[4 * c] = fmaf(w[u], x[u][c].x, a[4 * c]);
+            a[4 * c + 1] = fmaf(w[u], x[u][c].y, a[4 * c + 1]);
+            a[4 * c + 2] = fmaf(w[u], x[u][c].z, a[4 * c + 2]);
+            a[4 * c + 3] = fmaf(w[u], x[u][c].w, a[4 * c + 3]);
+          }
+    }
+  };
+  add(aw, 0, p.win_slots);
+  add(a2, p.win_slots, nslots);
+#pragma unroll
+  for (int c = 0; c < kVec; ++c) {
+    const int ch = 4 * (kPer * c + j);
+    *reinterpret_cast<float4*>(&ow[r][ch]) =
         make_float4(aw[4 * c] * inv, aw[4 * c + 1] * inv, aw[4 * c + 2] * inv, aw[4 * c + 3] * inv);
-    // the un-rotation runs on fp16 operands (2^-12 of a value each); with the
+    // the un-rotation runs on fp16 operands (2^-11 of a value each); with the
     // rotation folded into the model the sums are the result and stay fp32
     if (p.fold_rv) {
-      float* d = &ow[r][32 * c + 4 * j];
+      float* d = &ow[r][ch];
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = fmaf(a2[4 * c + e], inv, d[e]);
     } else {
-      *reinterpret_cast<uint2*>(&ox[r][32 * c + 4 * j]) =
-          make_uint2(f2_to_h2_bits(a2[4 * c] * inv, a2[4 * c + 1] * inv),
-                     f2_to_h2_bits(a2[4 * c + 2] * inv, a2[4 * c + 3] * inv));
+      *reinterpret_cast<uint2*>(&ox[r][ch]) = make_uint2(f2_to_h2_bits(a2[4 * c] * inv, a2[4 * c + 1] * inv),
+                                                         f2_to_h2_bits(a2[4 * c + 2] * inv, a2[4 * c + 3] * inv));
     }
   }
   __syncthreads();
@@ -871,9 +1169,9 @@ __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreePar
 
 template <int NG>
 cudaError_t set_attrs() {
-  cudaError_t e = cudaFuncSetAttribute(oscar_tree_attn_kernel<NG, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem(1));
+  cudaError_t e = cudaFuncSetAttribute(oscar_tree_attn_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(oscar_tree_attn_kernel<NG, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem(2));
+    e = cudaFuncSetAttribute(oscar_tree_pair_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   return e;
 }
 
@@ -896,18 +1194,22 @@ cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t s) {
   const bool wide = p.tile_rows == 2 * kWideRows;
   cudaError_t e = launch_pdl(wide ? oscar_tree_rotate_kernel<true> : oscar_tree_rotate_kernel<false>, dim3(p.row_tiles, p.num_kv_heads, p.batch), dim3(kRotThreads),
                              kRotSmem, s, p);
-  const dim3 grid(p.col_tiles * nslots, p.num_kv_heads, p.batch);
-  const bool one = p.tile_rows == 16;
-  if (e == cudaSuccess && wide) e = launch_tree_wide(p, s);
-  if (e == cudaSuccess && !wide)
-    e = p.ngroups == kGroups
-            ? launch_pdl(one ? oscar_tree_attn_kernel<kGroups, 1> : oscar_tree_attn_kernel<kGroups, 2>, grid,
-                         dim3(kThreads), tree_smem(one ? 1 : 2), s, p)
-            : launch_pdl(one ? oscar_tree_attn_kernel<2, 1> : oscar_tree_attn_kernel<2, 2>, grid, dim3(kThreads),
-                         tree_smem(one ? 1 : 2), s, p);
+  if (e == cudaSuccess) {
+    if (wide)
+      e = launch_tree_wide(p, s);
+    else if (p.tile_rows == 16)
+      e = launch_pdl(p.ngroups == kGroups ? oscar_tree_attn_kernel<kGroups> : oscar_tree_attn_kernel<2>,
+                     dim3(p.col_tiles * nslots, p.num_kv_heads, p.batch), dim3(kThreads), kTreeSmem, s, p);
+    else
+      e = launch_pdl(p.ngroups == kGroups ? oscar_tree_pair_kernel<kGroups> : oscar_tree_pair_kernel<2>,
+                     dim3(2 * p.win_slots + p.splits, p.num_kv_heads, p.batch), dim3(kThreads), kPairSmem, s, p);
+  }
   if (e == cudaSuccess)
-    e = launch_pdl(oscar_tree_merge_kernel, dim3((rows + kMergeRows - 1) / kMergeRows, p.num_kv_heads, p.batch),
-                   dim3(kMergeThreads), nslots * kMergeRows * 4, s, p);
+    e = (int64_t)rows * p.num_kv_heads * p.batch <= kMergeFewRows
+            ? launch_pdl(oscar_tree_merge_kernel<4>, dim3((rows + 3) / 4, p.num_kv_heads, p.batch), dim3(kMergeThreads),
+                         nslots * 4 * 4, s, p)
+            : launch_pdl(oscar_tree_merge_kernel<kMergeRows>, dim3((rows + kMergeRows - 1) / kMergeRows, p.num_kv_heads, p.batch),
+                         dim3(kMergeThreads), nslots * kMergeRows * 4, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

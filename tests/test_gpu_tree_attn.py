@@ -103,6 +103,73 @@ def test_more_pages_than_one_batch_of_ids():
     _check(layer, [12000], 5, 2)
 
 
+# Many requests of 17 .. 32 query rows per cached head take another kernel, whose warps share
+# page pairs: 10 requests x 8 heads are more than one wave of 16-row tiles on 152 SMs.
+_MANY = [700, 0, 3, 68, 69, 84, 85, 260, 333, 196]
+
+
+@pytest.mark.parametrize("hq,t", [(8, 17), (8, 32), (16, 9), (16, 16), (32, 5), (64, 3), (64, 4)])
+def test_many_requests(hq, t):
+    layer = _layer(_MANY, hq, 8, 4, 64, 10, 704, seed=23)
+    _check(layer, _MANY, t, 3, seed=t)
+
+
+@pytest.mark.parametrize("group,fold", [(32, 1), (64, 0), (64, 1)])
+def test_many_ragged_requests(group, fold):
+    # some use 16 rows or fewer, one none
+    used = [11, 11, 1, 9, 8, 5, 0, 10, 4, 3]
+    layer = _layer(_MANY, 16, 8, 4, 64, 10, 704, seed=24, group=group, fold_rv=fold)
+    _check(layer, _MANY, 11, 3, used)
+
+
+@pytest.mark.parametrize("splits", [1, 3, 40, 256])
+def test_many_requests_split(splits):
+    # one split of the longest: 70 pages for each warp, three batches of page ids
+    lengths = [9000] + _MANY[1:]
+    layer = _layer(lengths, 16, 8, 4, 64, 10, 9040, seed=25, num_splits=splits)
+    _check(layer, lengths, 9, 2)
+
+
+def test_many_requests_token_spikes():
+    layer = _layer(_MANY, 16, 8, 4, 64, 10, 704, seed=26, spikes=True)
+    _check(layer, _MANY, 12, 3)
+
+
+def test_many_requests_bad_page_ids_and_replay():
+    layer = _layer([400] * 10, 16, 8, 4, 64, 10, 512, seed=27)
+    host, dev = draft(layer, 10, 9, 0)
+    par = torch.tensor([[-1, 0, 0, 1, 2, 2, 3, 6, 7]] * 10, dtype=torch.int32, device="cuda")
+    good = tree_call(layer, dev, par)
+    ws = torch.empty(layer.ctx.tree_attn_workspace_bytes(10, 9), dtype=torch.uint8, device="cuda")
+    pt, state, o = layer.cache.page_table[:10].clone(), layer.cache.state[:10], torch.zeros_like(dev[0])
+    call = lambda: layer.ctx.tree_attn(*dev, par, pt, state, o, 10, 9, ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(o, good)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, good) and layer.ctx.error_flags() == 0
+    pt[4, 5], pt[4, 6] = layer.cache.num_pages, -4
+    graph.replay()
+    torch.cuda.synchronize()
+    assert layer.ctx.error_flags() == abi.FLAG_BAD_PAGE_ID
+    assert torch.equal(o[:4], good[:4]) and torch.equal(o[5:], good[5:])
+    # the positions of those pages take no part, whatever they hold
+    pages = layer.cache.pool.view(layer.cache.num_pages, -1)
+    for i in (5, 6):
+        pages[int(layer.cache.page_table_host[4, i])] = 0xFF
+    pt[4, 5:7] += 2 * layer.cache.num_pages
+    skipped = o[4].clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert layer.ctx.error_flags() == abi.FLAG_BAD_PAGE_ID
+    assert torch.equal(o[4], skipped) and torch.isfinite(o).all() and not torch.equal(o[4], good[4])
+
+
 def test_fold_rv():
     layer = _layer([400], 8, 2, 4, 64, 1, 512, seed=12, fold_rv=1)
     _check(layer, [400], 9, 2)
