@@ -261,15 +261,17 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_commit_draft_kernel(CommitP
         if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
     }
     // the last of a request's 2 Hkv CTAs to have read its state publishes the new one: each
-    // reads it before taking its ticket
+    // reads it before taking its ticket. The counters belong to window rows and wrap to 0, so
+    // calls on other requests may run at the same time
     if (lane == 0 && request(warp) < p.batch) {
-      const int b = request(warp);
-      asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
-      if (atomicAdd(p.tickets + b, 1u) == 2u * Hkv - 1u) {
+      if (bad) {
+        if (h == 0 && kind == 0) atomicOr(p.err_flags, bad);
+      } else {
         asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
-        if (bad) atomicOr(p.err_flags, bad);
-        else p.state[b] = out;
-        p.tickets[b] = 0u;
+        if (atomicInc(p.tickets + out.window_row, 2u * Hkv - 1u) == 2u * Hkv - 1u) {
+          asm volatile("fence.acq_rel.gpu;\n" ::: "memory");
+          p.state[request(warp)] = out;
+        }
       }
     }
   }

@@ -35,7 +35,7 @@ struct oscar_ctx {
   __half* rv16 = nullptr;       // R_V in fp16 (the tree attention's un-rotation operand)
   uint32_t* qrec = nullptr;
   float* part = nullptr;
-  uint32_t* tickets = nullptr;  // per request of a commit: CTAs that have read its state
+  uint32_t* tickets = nullptr;  // per window row: CTAs of a commit that have read its request's state
   uint32_t* flags = nullptr;    // [0] error flags, [1] append ticket counter
   int max_splits = 0;
   bool loaded = false;

@@ -215,7 +215,7 @@ struct CommitParams {
   const float* clip_K;
   const float* clip_V;
   int32_t num_kv_heads, sink, recent, ngroups, fold_rv, max_batch, batch, nodes;
-  uint32_t* tickets;        // [max_batch], zero between launches
+  uint32_t* tickets;        // [max_batch], by window row, zero between launches
   uint32_t* err_flags;
 };
 

@@ -318,7 +318,8 @@ int oscar_tree_attn(oscar_ctx* ctx, const void* q, const void* k, const void* v,
  * DEVICE int32 [batch], 0 .. n_draft, as oscar_verify_draft writes them;
  * page_table and state as for oscar_quant_append: page_table must map every
  * position below the new int2_end. A request with a count or row index out of
- * range sets OSCAR_FLAG_BAD_TREE and keeps its cache and state. Statuses as for
+ * range sets OSCAR_FLAG_BAD_TREE and keeps its cache and state. Calls that may
+ * overlap on the GPU must be on different requests (window rows). Statuses as for
  * oscar_tree_attn. */
 int oscar_commit_draft(oscar_ctx* ctx, const int32_t* page_table, oscar_seq_state* state, const void* k,
                        const void* v, const int32_t* path, const int32_t* n_path, int32_t batch, int32_t n_draft,

@@ -153,6 +153,34 @@ def test_captured_and_replayed():
     _same(ref, com)
 
 
+def test_two_streams_and_repeated_rows():
+    # two commits of one context at the same time, on different requests; a row may be
+    # taken twice
+    lengths = [70 + 31 * i for i in range(12)]
+    ref, com = _twins(lengths, 8, 8, 4, 64, 12, 600, seed=39, n_cal=128)
+    t = 6
+    path = torch.tensor([[0, 2, 2, 5, 5, 5]] * 12, dtype=torch.int32, device="cuda")
+    for layer in (ref, com):
+        for r in range(12):
+            layer.cache.reserve(r, 520, upload=False)
+        layer.cache.upload()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in range(6):
+        k, v = _rows(ref, 12, t, s)
+        count = torch.tensor([(5 * r + s) % (t + 1) for r in range(12)], dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for i, stream in enumerate(streams):
+            a = slice(6 * i, 6 * i + 6)
+            com.ctx.commit_draft(com.cache.page_table[a], com.cache.state[a], k[a], v[a], path[a], count[a], 6, t, stream=stream)
+        for r, n in enumerate(count.tolist()):
+            if n:
+                rows = path[r, :n].long()
+                ref.ctx.quant_append(ref.cache.page_table[r:], ref.cache.state[r:], k[r][rows].contiguous(),
+                                     v[r][rows].contiguous(), 1, n)
+        torch.cuda.synchronize()
+        _same(ref, com)
+
+
 def test_refusals():
     ref, _ = _twins([10], 4, 2, 4, 64, 1, 100, seed=38)
     k, v = _rows(ref, 1, 4, 0)
