@@ -430,12 +430,18 @@ __device__ void window_tile(const TreeParams& p, Shared& sm, const Work& wk, int
   wm::cp_wait<0>();
 }
 
-// the issuing warp of group g: its jobs g, g + 2, ..., each in two halves of 64 tokens, so
-// that one half's products run while the softmax works on the other. Descriptors are
-// prepared once, a step along an operand adds a constant to the low word.
+// The issuing warp of group g: its jobs g, g + 2, ..., the values (and with two row tiles the
+// scores) in two halves of 64 tokens, so that one half's products run while the softmax
+// works on the other. Descriptors are prepared once, a step along an operand adds a constant
+// to the low word.
+// whole: the scores of a job in one run of products, with one row tile. A change of product
+// shape or operand costs about 250 cycles, and the other group's softmax covers the longer
+// wait (1 x 32779 tokens, 104 rows: 47.5 us against 50.5). With two row tiles the wait is
+// the longer of the two (8 x 16k tokens, 488 rows: 505 us against 569).
+template <bool whole>
 __device__ void issue_products(Shared& sm, const Work& wk, uint32_t tmem, int g, uint32_t lead) {
   volatile int* abort = &sm.abort;
-  const uint32_t id = idesc(!wk.int2, 128), id_s = idesc(!wk.int2, 64);
+  const uint32_t id = idesc(!wk.int2, 128), id_s = whole ? id : idesc(!wk.int2, 64);
   const uint8_t* qs = wk.nrt == 2 && g ? sm.q2 : sm.q;
   const uint64_t dq = sw128_desc(smem_u32(qs)), dqx = plain_desc(smem_u32(qs) + kWideImage);
   const uint64_t dk = sw128_desc(smem_u32(sm.k[0])), dv = sw128_desc(smem_u32(sm.v[0])), dx = plain_desc(smem_u32(sm.kx[0]));
@@ -459,10 +465,11 @@ __device__ void issue_products(Shared& sm, const Work& wk, uint32_t tmem, int g,
     if (wk.int2)
       umma_ss(s + 64 * half, dqx, dx + (uint32_t)st * (kWideExtra >> 4) + (uint32_t)half * (1024 >> 4), id_s, 1u, lead);
     commit_lead(&sm.sfull[g][half], lead);
-    if (half) commit_lead(&sm.kfree[st], lead);
+    if (whole) commit_lead(&sm.sfull[g][1], lead);
+    if (half || whole) commit_lead(&sm.kfree[st], lead);
     return true;
   };
-  bool ok = g >= wk.njobs || (scores(g, 0) && scores(g, 1));
+  bool ok = g >= wk.njobs || (scores(g, 0) && (whole || scores(g, 1)));
   for (int j = g; ok && j < wk.njobs; j += 2) {
     const int t = wk.tile_of(j), st = t & 1;
     for (int half = 0; ok && half < 2; ++half) {
@@ -481,7 +488,7 @@ __device__ void issue_products(Shared& sm, const Work& wk, uint32_t tmem, int g,
       commit_lead(&sm.ofull[g], lead);
       if (half) commit_lead(&sm.vfree[st], lead);
       // its S is overwritten only now: one warp's products run in issue order
-      if (j + 2 < wk.njobs) ok = scores(j + 2, half);
+      if (j + 2 < wk.njobs && (half || !whole)) ok = scores(j + 2, whole ? 0 : half);
     }
   }
   if (!ok) *abort = 1;
@@ -772,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1) oscar_tree_wide_kernel(TreeParams
 
   float m = -INFINITY, l = 0.f, unit = p.scale_log2;
   if (warp >= kMmaWarp) {
-    issue_products(sm, wk, tmem, warp - kMmaWarp, lane == 0);
+    if (wk.nrt == 1) issue_products<true>(sm, wk, tmem, warp - kMmaWarp, lane == 0);
+    else issue_products<false>(sm, wk, tmem, warp - kMmaWarp, lane == 0);
   } else if (warp >= kSoftWarps) {
     const int w = warp - kSoftWarps;
     if (wk.int2) {
