@@ -623,16 +623,22 @@ static TreePlan tree_plan(const oscar_ctx* ctx, int batch, int nodes) {
     tiles(2 * kWideRows);
     s = std::max(one_wave(1), (pages + kSplitPages - 1) / kSplitPages);
   } else {
-    // Warp tiles. A call whose single wave leaves a CTA at most 128 pages is bound by latency
-    // and takes 16-row tiles (1 x 4099 tokens, 20 rows: 19.2 us against 21.4); else 17 .. 32
-    // rows go to the pair kernel (28 x 100k, 32 rows: 1346 us against 1538), in about five
-    // waves, so that ragged requests and the last wave leave few SMs idle.
+    // Warp tiles. A call whose single wave leaves a CTA at most 120 pages is bound by latency
+    // and takes 16-row tiles (1 x 4099 tokens, 32 rows: 20 us against 23; 1 x 32768, 114 pages:
+    // 34 against 38; 4 x 3900, 123 pages: 32.5 against 29.5); else 17 .. 32 rows go to the pair kernel (28 x 100k, 32 rows: 1240 us
+    // against 1511; 16 ragged requests of 8k to 32k: 175 against 180).
     tiles(16);
     s = one_wave(2);
-    if (s < 1 || pages > 128 * s) {
+    if (s < 1 || pages > 120 * s) {
+      // One wave while it has 8 splits or more for each unit (2 x 32768 tokens, 32 rows: 51 us
+      // against 78 with five waves; 4 x 50k: 120 against 140). More units than that leave a
+      // part of the wave empty, and ragged requests more: up to five waves, of 128 pages or
+      // more each (8 x 32768: 153 us against 163 of 85 pages; 16 x 16384: 169 against 176).
       tiles(t.rows <= 16 ? 16 : 32);
       const int64_t units = (int64_t)batch * hkv * t.col_tiles;
-      s = std::max({one_wave(2), (10 * (int64_t)ctx->num_sms + units - 1) / units, (pages + kSplitPages - 1) / kSplitPages});
+      s = one_wave(2);
+      if (s < 8) s = std::max(s, std::min((10 * (int64_t)ctx->num_sms + units - 1) / units, pages / 128));
+      s = std::max(s, (pages + kSplitPages - 1) / kSplitPages);
     }
   }
   s = std::min<int64_t>(s, (pages + 7) / 8);   // >= 8 pages per split: one per warp
