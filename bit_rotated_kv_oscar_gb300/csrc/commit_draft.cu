@@ -12,13 +12,15 @@
 // CTA (x, h, kind) takes the keys or the values of KV head h of requests x, x + gridDim.x,
 // ..., sixteen at a time: one warp reads and checks one request's state, count and path. The
 // rotation (64 KiB) is staged in shared memory once, two CTAs per SM, and the rows that
-// all of these requests quantise are rotated sixteen at a time, eight to a thread, so that
-// one shared-memory read of a rotation entry feeds eight FMAs; the next sixteen are on
-// their way meanwhile. The sums keep the append kernel's order (two chains of 64 terms per
-// channel, then their sum), which the byte equality needs.
+// all of these requests quantise are rotated sixteen at a time, eight rows by two channels to
+// a thread; the next sixteen are on their way meanwhile. The sums keep the append kernel's
+// order (two chains of 64 terms per channel, then their sum), which the byte equality needs
+// and which leaves the tensor cores out.
 //
-// Bound: latency (state, rows, rotation, stores follow one another); the rotation itself is
-// 4 * 128 * 128 flops per row and head.
+// Bound: latency for one request (7.5 us with the launch; state, rows, rotation and stores
+// follow one another). 64 requests, 552 rows, 8 heads: 29 us, of which 6 remain without rows
+// to quantise; the rest is two or three rounds of sixteen rows for a CTA, about 5 us of
+// rotation (shared-memory reads) and 4 us of fetch, quantisation and stores each.
 #include <type_traits>
 
 #include "oscar_internal.cuh"
@@ -31,6 +33,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kReqs = kThreads / 32;        // requests read at once
 constexpr int kRows = 16;                   // rows rotated at once
+static_assert(kRows == kThreads / 32, "a warp stores a row");
 constexpr int kMat = kHeadDim * kHeadDim;
 struct CommitSmem {
   float rot[kMat];                          // R_K[h] or R_V[h]
@@ -42,7 +45,7 @@ struct CommitSmem {
   int path[kReqs][kTreeNodes];
   int n[kReqs], L[kReqs], E[kReqs], row[kReqs];   // accepted rows, state and window row; n = 0: nothing to do
   int first[kReqs + 1];                     // rows to quantise before each request
-  int page[2][kRows];                       // page ids of the rows in raw
+  int page[2][kRows], slot[2][kRows];       // page ids of the rows in raw, and their places in them
 };
 
 __global__ void __launch_bounds__(kThreads, 2) oscar_commit_draft_kernel(CommitParams p) {
@@ -118,26 +121,26 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_commit_draft_kernel(CommitP
     }
     __syncthreads();
     const int M = sm.first[kReqs];
-    auto request_of = [&](int r) {   // of row r of the M
-      int q = 0;
-      while (r >= sm.first[q + 1]) ++q;
-      return q;
-    };
-    auto fetch = [&](int r0, int buf) {   // rows r0 .. of the M: 16-byte pieces
-      for (int i = tid; i < min(kRows, M - r0) * 16; i += kThreads) {
-        const int r = i >> 4, c = 8 * (i & 15), q = request_of(r0 + r);
-        const int pos = sm.E[q] + (r0 + r - sm.first[q]), L = sm.L[q];
-        const __nv_bfloat16* src =
-            pos < L ? window_of(q) + (size_t)(S + pos % W) * kHeadDim + c
-                    : input + (((size_t)request(q) * p.nodes + sm.path[q][pos - L]) * Hkv + h) * kHeadDim + c;
-        wm::cp_async16((uint32_t)__cvta_generic_to_shared(&sm.raw[buf][r][c]), src);
-        if ((i & 15) == 0) {
-          const int pidx = pos / kPage;
-          if (pidx < p.pt_stride)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"((uint32_t)__cvta_generic_to_shared(&sm.page[buf][r])),
-                         "l"(p.page_table + (size_t)request(q) * p.pt_stride + pidx));
-          else
-            sm.page[buf][r] = -1;
+    auto fetch = [&](int r0, int buf) {   // rows r0 .. of the M: a half-warp a row, 16-byte pieces
+      if (tid < kRows * 16) {
+        const int r = tid >> 4, c = 8 * (tid & 15), at = r0 + r;
+        const uint32_t before = __ballot_sync(0xffffffffu, at >= sm.first[(lane & 15) + 1]);
+        const int q = __popc((before >> (lane & 16)) & 0xffffu);   // its request
+        if (at < M) {
+          const int pos = sm.E[q] + (at - sm.first[q]), L = sm.L[q];
+          const __nv_bfloat16* src =
+              pos < L ? window_of(q) + (size_t)(S + pos % W) * kHeadDim + c
+                      : input + (((size_t)request(q) * p.nodes + sm.path[q][pos - L]) * Hkv + h) * kHeadDim + c;
+          wm::cp_async16((uint32_t)__cvta_generic_to_shared(&sm.raw[buf][r][c]), src);
+          if ((tid & 15) == 0) {
+            const int pidx = pos / kPage;
+            sm.slot[buf][r] = pos % kPage;
+            if (pidx < p.pt_stride)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"((uint32_t)__cvta_generic_to_shared(&sm.page[buf][r])),
+                           "l"(p.page_table + (size_t)request(q) * p.pt_stride + pidx));
+            else
+              sm.page[buf][r] = -1;
+          }
         }
       }
       wm::cp_commit();
@@ -160,30 +163,39 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_commit_draft_kernel(CommitP
       }
       __syncthreads();
       {
-        // thread (rows 8 g .., half, channel c): 64 terms of x R in order, for each row
-        const int g = tid >> 8, half = (tid >> 7) & 1, c = tid & 127, k0 = 64 * half, n = rows - 8 * g;
+        // thread (rows 8 g .., half, channels c, c + 1): 64 terms of x R in order, for each.
+        // Half of the threads: what counts is shared-memory reads per product, and 16 sums
+        // a thread halve those of x (64 requests, 552 rows: 32 us against 36)
+        const int g = tid >> 7, half = (tid >> 6) & 1, c = 2 * (tid & 63), k0 = 64 * half, n = rows - 8 * g;
         if (fold) {
-          for (int r = 8 * g; r < min(rows, 8 * g + 8); ++r) sm.red[r][half][c] = half ? 0.f : sm.x[r][c];
-        } else if (n > 0) {
+          if (g < 2)
+            for (int r = 8 * g; r < min(rows, 8 * g + 8); ++r)
+              *reinterpret_cast<float2*>(&sm.red[r][half][c]) =
+                  half ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(&sm.x[r][c]);
+        } else if (g < 2 && n > 0) {
           const float* R = sm.rot + k0 * kHeadDim + c;
           auto rotate = [&](auto count) {
             constexpr int N = decltype(count)::value;
-            float acc[N] = {};
-#pragma unroll 4
+            float2 acc[N] = {};
+#pragma unroll 2
             for (int i = 0; i < 64; i += 4) {
-              const float v0 = R[i * kHeadDim], v1 = R[(i + 1) * kHeadDim], v2 = R[(i + 2) * kHeadDim],
-                          v3 = R[(i + 3) * kHeadDim];
+              float2 v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float2*>(R + (i + e) * kHeadDim);
 #pragma unroll
               for (int r = 0; r < N; ++r) {
                 const float4 x = *reinterpret_cast<const float4*>(&sm.x[8 * g + r][k0 + i]);
-                acc[r] = fmaf(x.x, v0, acc[r]);
-                acc[r] = fmaf(x.y, v1, acc[r]);
-                acc[r] = fmaf(x.z, v2, acc[r]);
-                acc[r] = fmaf(x.w, v3, acc[r]);
+                const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  acc[r].x = fmaf(xs[e], v[e].x, acc[r].x);
+                  acc[r].y = fmaf(xs[e], v[e].y, acc[r].y);
+                }
               }
             }
 #pragma unroll
-            for (int r = 0; r < N; ++r) sm.red[8 * g + r][half][c] = acc[r];   // rows past the last are not used
+            for (int r = 0; r < N; ++r)   // rows past the last are not used
+              *reinterpret_cast<float2*>(&sm.red[8 * g + r][half][c]) = acc[r];
           };
           if (n > 4) rotate(std::integral_constant<int, 8>());
           else if (n > 1) rotate(std::integral_constant<int, 4>());
@@ -225,14 +237,14 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_commit_draft_kernel(CommitP
         }
       }
       __syncthreads();
-      for (int r = tid >> 7; r < rows; r += kThreads / 128) {
-        const int role = tid & 127;
+      if (warp < rows) {   // a warp per row
         // the roles of this kind: K codes 0 .. 7, metadata 64 .. 67; V codes 32 .. 47, metadata 68 .. 71
-        if (kind ? (role >= 32 && role < 48) || (role >= 68 && role < 72) : role < 8 || (role >= 64 && role < 68)) {
-          const int q = request_of(r0 + r), pos = sm.E[q] + (r0 + r - sm.first[q]), id = sm.page[buf][r];
+        const int r = warp, ncodes = kind ? 16 : 8, role = lane < ncodes ? 32 * kind + lane : 64 + 4 * kind + lane - ncodes;
+        if (lane < ncodes + 4) {
+          const int id = sm.page[buf][r];
           if (id >= 0 && id < p.num_pages)
-            store_token_block(p.pool + ((size_t)id * Hkv + h) * block_bytes(ng), pos % kPage, role, ng, sm.codes[r], sm.meta[r]);
-          else if (role == 0 || role == 32)
+            store_token_block(p.pool + ((size_t)id * Hkv + h) * block_bytes(ng), sm.slot[buf][r], role, ng, sm.codes[r], sm.meta[r]);
+          else if (lane == 0)
             atomicOr(p.err_flags, OSCAR_FLAG_BAD_PAGE_ID);
         }
       }
