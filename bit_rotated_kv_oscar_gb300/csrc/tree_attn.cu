@@ -19,7 +19,9 @@
 //      mma operand fragments (fp16, one power-of-two scale per tile).
 //   2. oscar_tree_attn_kernel    grid (row tiles x (window chunks + splits), Hkv, B):
 //      the INT2 CTAs stream a slice of the pages, the others attend over 128 tokens
-//      of sink, ring and tree; one partial row (sum, maximum, denominator) each.
+//      of sink, ring and tree; one partial row (sum, maximum, denominator) each. More rows:
+//      oscar_tree_pair_kernel for 17 .. 32, oscar_tree_wide_kernel (tree_attn_wide.cu) past
+//      32; the choice and its figures are at tree_plan in oscar_api.cu.
 //   3. oscar_tree_merge_kernel   log-sum-exp merge, R_V^T, normalisation, bf16.
 #include "int2_page.cuh"
 #include "tree_attn.cuh"
@@ -691,10 +693,14 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_tree_attn_kernel(TreeParams
 // 2b. the same for 17 .. 32 query rows: two warps share a page pair. Each scores its own
 //     page for all 32 rows and hands its probabilities to the other; each adds both
 //     pages' values for its half of the channels. A warp then holds 64 value sums per
-//     lane instead of 128, so four warps fit a scheduler instead of two (the 128-register
-//     layout above is bound by the latency of its two warps: 41 % issue, 48 % tensor).
-//     The scores take dequantised keys (s c 2^m, 3 s rounded to fp16; the zero points
-//     enter as above), which saves the group sums' scaling.
+//     lane instead of 128, so four warps fit a scheduler instead of two. The scores take
+//     dequantised keys (s c 2^m, 3 s rounded to fp16; the zero points enter as above), which
+//     saves the group sums' scaling.
+//     Measured (28 x 100k tokens, 8 heads, 32 rows): 1240 us; two 16-row tiles, which read
+//     and unpack each page twice, 1511; 32 rows in one warp 1443. A page takes 70 products of
+//     8 cycles on a scheduler's tensor pipe (646 us in all); the pipe is busy half of the
+//     time, the issue slots too (44 %): what is left are the dependences of four warps. Copies
+//     from HBM would take 320 us.
 // --------------------------------------------------------------------------
 constexpr int kPairs = kWarps / 2;
 struct PairSmem {
@@ -702,7 +708,7 @@ struct PairSmem {
   uint4 q[2 * 8 * 32];
   uint4 P[kWarps][2][32];
   float mx[kWarps][32];
-  // read again at each page: they would not fit the registers
+  // read again at each page: in registers they spill others (1415 us against 1240, below)
   uint2 zs[2][32];
   float unit, tau, lg_ps;
   uint32_t mul, zmul;

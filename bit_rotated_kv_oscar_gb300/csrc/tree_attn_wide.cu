@@ -10,8 +10,8 @@
 //     gives lane (a, b) the code words of tokens a, a + 8 and channels 2 b, 2 b + 1
 //     (mod 8), whose fp16 pairs land in 32 different banks for every store. Raw pages
 //     arrive by cp.async.
-//   2 warps, one per softmax group, issue the products: S = Q~ K^T, 128 x 128 x 144, and O += P V^, 128 x 128 x
-//     128, P in tensor memory. The 16 further reduction columns of S are the keys' zero
+//   2 warps, one per softmax group, issue the products: S = Q~ K^T, 128 x 128 x 144, and
+//     O += P V^, 128 x 128 x 128, P in tensor memory. The 16 further reduction columns of S are the keys' zero
 //     points against the group sums of q~ (hi and lo parts), so only q~ and 3 s are
 //     rounded.
 //   2 groups of 4 softmax warps, thread = row: P = 2^(S - max) in fp16 over S. With more
@@ -24,7 +24,16 @@
 // The BF16 part (sink, ring and the tree's own nodes) is the same computation in the raw
 // basis on bf16 operands; its probabilities are split into two bf16 parts.
 //
-// What bounds it: see the figures at the launcher.
+// What bounds it: 8 requests x 16k tokens x 8 heads, 488 rows (two row tiles): 505 us, of
+// which 418 remain without the products; the tensor pipe alone would take 125 us at full
+// rate, but a run of products of another shape or operand starts about 250 cycles after the
+// one before it, four times per row tile and 128 tokens. The rest is the softmax (a lane's
+// 128 exponentials, their sums and conversions, and the tensor-memory traffic) with eight
+// dequantising warps on the same four schedulers. One request of 32779 tokens, 104 rows:
+// 48 us for rotation, this kernel and the merge. Warp tiles of 32 rows took 1063 and
+// 93 us there: they unpack a page again for each tile, here once for 256 rows.
+// Requests of 17 .. 32 rows are faster there (28 x 100k tokens: 1240 us against 1670): a tile
+// of 128 rows is then three quarters copies.
 #include "int2_page.cuh"
 #include "tc_ptx.cuh"
 #include "tree_attn.cuh"

@@ -18,8 +18,11 @@
 // on any launch shape. One probability is off by at most 2^-45, far below fp32.
 //
 // Bound: HBM, the last node's row of p (and q) once: a cluster of CTAs shares a
-// request's row, each warp sums one contiguous piece, and only the warp that holds
-// the token reads its piece again (from L2).
+// request's row, each warp sums one contiguous piece, and only the CTA that holds
+// the token reads one warp's piece again (from L2). Measured: 64 requests of 26 nodes over
+// 151936 tokens 20.4 us (the rows alone 5.7 at the copy rate); one request 8.7 us: the
+// tree's loads, the probabilities of its tokens, the row, two cluster barriers and the
+// search follow one another.
 #include "oscar_internal.cuh"
 #include "warp_mma.cuh"
 
