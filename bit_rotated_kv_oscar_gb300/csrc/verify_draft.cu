@@ -82,7 +82,7 @@ __device__ __forceinline__ void load4(const float* row, int at, int lo, int hi, 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) oscar_verify_draft_kernel(VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 2) oscar_verify_draft_kernel(VerifyParams p) {
   const int C = p.ctas, rank = blockIdx.x % C, b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.nodes, V = p.vocab;
   __shared__ int s_par[kTreeNodes], s_tok[kTreeNodes];
@@ -361,9 +361,12 @@ cudaError_t launch_verify_draft(const VerifyParams& p, cudaStream_t s) {
     int n = 0;
     return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0 ? n : 1;
   });
-  // about four CTAs per SM in all, at least 2048 entries each, at most 16 to a cluster
+  // one wave of two CTAs per SM where the batch leaves the choice, at least 2048 entries each,
+  // at most 16 to a cluster: every CTA waits through the same chain of loads (64 requests,
+  // 151936 tokens, rows not in L2: 17.9 us; 1.7 waves of half the entries 25, three CTAs of
+  // fewer registers 21.6)
   int c = 1;
-  while (c < 16 && (int64_t)2 * c * p.batch <= 4 * num_sms && p.vocab / (2 * c) >= 2048) c *= 2;
+  while (c < 16 && (int64_t)2 * c * p.batch <= 2 * num_sms && p.vocab / (2 * c) >= 2048) c *= 2;
   VerifyParams q = p;
   q.ctas = c;
   cudaLaunchConfig_t cfg = {};
