@@ -19,10 +19,13 @@
 //
 // Bound: HBM, the last node's row of p (and q) once: a cluster of CTAs shares a
 // request's row, each warp sums one contiguous piece, and only the CTA that holds
-// the token reads one warp's piece again (from L2). Measured: 64 requests of 26 nodes over
-// 151936 tokens 20.4 us (the rows alone 5.7 at the copy rate); one request 8.7 us: the
-// tree's loads, the probabilities of its tokens, the row, two cluster barriers and the
-// search follow one another.
+// the token reads one warp's piece again (from L2). Measured, rows not in L2: 64 requests
+// of 26 nodes over 151936 tokens 16.7 us (the rows alone 5.7 at the copy rate), of which 4 are
+// the walk and 3 the search; 256 requests over 32003 tokens against the draft's own
+// distributions 17.6 (9.7); one request 9.0: the tree's loads, the probabilities of its
+// tokens, the row, two cluster barriers and the search follow one another.
+#include <type_traits>
+
 #include "oscar_internal.cuh"
 #include "warp_mma.cuh"
 
@@ -44,11 +47,15 @@ struct Fix {
   int hi, lo;   // hi * 2^23 + lo, |lo| <= 2^22
   __device__ __forceinline__ long long value() const { return ((long long)hi << 23) + lo; }
 };
-__device__ __forceinline__ Fix split(float p) {
-  p = fminf(fmaxf(p, 0.f), 1.f);
+constexpr int kHi0 = 0x40c00000, kLo0 = 0x35400000;   // 6 and 1.5 * 2^-21
+__device__ __forceinline__ Fix split_raw(float p) {   // of a clamped p: hi + kHi0, lo + kLo0
   const float u = __fadd_rn(p, 6.f);
   const float v = __fadd_rn(__fsub_rn(p, __fsub_rn(u, 6.f)), 0x1.8p-21f);
-  return {__float_as_int(u) - 0x40c00000, __float_as_int(v) - 0x35400000};
+  return {__float_as_int(u), __float_as_int(v)};
+}
+__device__ __forceinline__ Fix split(float p) {
+  const Fix f = split_raw(__saturatef(p));
+  return {f.hi - kHi0, f.lo - kLo0};
 }
 __device__ __forceinline__ u64 fix(float p) { return (u64)split(p).value(); }
 __device__ __forceinline__ u64 warp_sum_u64(u64 x) {
@@ -210,42 +217,61 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_verify_draft_kernel(VerifyP
       }
     };
     u64 sum = 0;
-    // four steps of 128 entries at a time, all loads before the first use; a warp whose
-    // steps reach past the row's ends takes them one by one
-    int at = w0 + 4 * lane;
-    if (!less || qvec) {
-      for (; w0 >= 0 && at - 4 * lane + 512 <= w1; at += 512) {
+    // four steps of 128 entries at a time, all loads before the first use; quads of entries
+    // that reach past the row's ends are left out here (one by one, the steps of a piece at
+    // a row's end set the time: 256 unaligned rows 23.7 us against 17.6)
+    auto pieces = [&](auto with_q) {
+      constexpr bool kLess = decltype(with_q)::value;
+      for (int at = w0 + 4 * lane; at - 4 * lane < w1; at += 512) {
         float4 x[4], y[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          x[u] = *reinterpret_cast<const float4*>(row + at + 128 * u);
-          if (less) y[u] = *reinterpret_cast<const float4*>(qrow + at + 128 * u);
+          const bool in = at + 128 * u >= 0 && at + 128 * u + 4 <= w1;
+          x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (in) x[u] = *reinterpret_cast<const float4*>(row + at + 128 * u);
+          if (kLess && in) y[u] = *reinterpret_cast<const float4*>(qrow + at + 128 * u);
         }
-        int hi = 0, lo = 0;   // at most 16 entries: |lo| < 2^26, hi < 2^26
+        int hi = 0, lo = 0;   // 16 entries: |lo| <= 2^27, hi <= 2^25
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
           const float ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const Fix f = split(xs[e]);
-            if (less) {
-              const Fix q = split(ys[e]);
-              const long long d = ((long long)(f.hi - q.hi) << 23) + (f.lo - q.lo);
-              sum += d > 0 ? (u64)d : 0;
+            const float a = __saturatef(xs[e]);
+            const Fix f = split_raw(a);
+            if constexpr (kLess) {
+              const float b = __saturatef(ys[e]);
+              const Fix q = split_raw(b);
+              if (a > b) {   // the rounding is monotone: the difference is 0 or more
+                hi += f.hi - q.hi;
+                lo += f.lo - q.lo;
+              }
             } else {
-              hi += f.hi;
-              lo += f.lo;
+              hi += f.hi - kHi0;
+              lo += f.lo - kLo0;
             }
           }
         }
-        if (!less) sum += (u64)(((long long)hi << 23) + lo);
+        sum += (u64)(((long long)hi << 23) + lo);
       }
-    }
-    for (; at < w1; at += 128) {
-      u64 f[4];
-      weights(at, f);
-      sum += (f[0] + f[1]) + (f[2] + f[3]);
+    };
+    if (less && !qvec) {
+      for (int at = w0 + 4 * lane; at < w1; at += 128) {
+        u64 f[4];
+        weights(at, f);
+        sum += (f[0] + f[1]) + (f[2] + f[3]);
+      }
+    } else {
+      if (less) pieces(std::true_type());
+      else pieces(std::false_type());
+      // the entries left out: of the quad that starts before the row (lanes 0 .. 3), and of the
+      // one that ends past it, if it is another (lanes 4 .. 7)
+      const int last = w1 - ((w1 + skew) & 3), i = lane < 4 ? w0 + lane : last + lane - 4;
+      if (lane < 4 ? w0 < 0 && i >= 0 && i < w1 : lane < 8 && last >= 0 && last >= w0 && i < w1) {
+        const u64 f = fix(row[i]), q = less ? fix(qrow[i]) : 0;
+        sum += f > q ? f - q : 0;
+      }
     }
     sum = warp_sum_u64(sum);
     if (without) {   // the children's tokens take no part (a repeated token's mass is 0 here)
@@ -363,8 +389,8 @@ cudaError_t launch_verify_draft(const VerifyParams& p, cudaStream_t s) {
   });
   // one wave of two CTAs per SM where the batch leaves the choice, at least 2048 entries each,
   // at most 16 to a cluster: every CTA waits through the same chain of loads (64 requests,
-  // 151936 tokens, rows not in L2: 17.9 us; 1.7 waves of half the entries 25, three CTAs of
-  // fewer registers 21.6)
+  // 151936 tokens: 17.9 us; 1.7 waves of half the entries 25, three CTAs of fewer
+  // registers 21.6)
   int c = 1;
   while (c < 16 && (int64_t)2 * c * p.batch <= 2 * num_sms && p.vocab / (2 * c) >= 2048) c *= 2;
   VerifyParams q = p;
