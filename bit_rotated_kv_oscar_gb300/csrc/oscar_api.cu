@@ -619,9 +619,11 @@ static TreePlan tree_plan(const oscar_ctx* ctx, int batch, int nodes) {
   int64_t s;
   if (t.rows > 32) {
     // tensor-memory kernel, one CTA per SM: its fixed cost (operands, 512 columns, merge of
-    // eight warps' rows) asks for long splits
+    // eight warps' rows) asks for long splits. Four of 128 pages or more leave few SMs idle in
+    // the last wave (16k tokens, 488 rows, 2 requests: 156 us against 215 with two splits, 5:
+    // 334 against 395, 8: 496 against 505; 104 rows, 4 requests: 90 against 123)
     tiles(2 * kWideRows);
-    s = std::max(one_wave(1), (pages + kSplitPages - 1) / kSplitPages);
+    s = std::max({one_wave(1), std::min<int64_t>(4, pages / 128), (pages + kSplitPages - 1) / kSplitPages});
   } else {
     // Warp tiles. A call whose single wave leaves a CTA at most 120 pages is bound by latency
     // and takes 16-row tiles (1 x 4099 tokens, 32 rows: 20 us against 23; 1 x 32768, 114 pages:

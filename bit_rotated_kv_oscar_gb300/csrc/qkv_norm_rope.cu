@@ -134,9 +134,12 @@ __global__ void __launch_bounds__(kThreads, 4) oscar_qkv_norm_rope_kernel(RopePa
 }  // namespace
 
 cudaError_t launch_qkv_norm_rope(const RopeParams& p, cudaStream_t s) {
+  // a token per CTA spreads few of them over the SMs (1000 tokens, 64 + 16 heads: 11.6 us
+  // against 21.6); from several waves on, 8 share a CTA's set-up (8192: 62.8 against 64.4)
   const int tpc = p.tokens >= 4096 ? kTokensPerCta : 1;
   const int64_t ctas = (p.tokens + tpc - 1) / tpc;
-  const cudaError_t e = launch_pdl(p.interleaved ? oscar_qkv_norm_rope_kernel<true> : oscar_qkv_norm_rope_kernel<false>, dim3((unsigned)ctas), dim3(kThreads), 0, s, p, tpc);
+  const cudaError_t e = launch_pdl(p.interleaved ? oscar_qkv_norm_rope_kernel<true> : oscar_qkv_norm_rope_kernel<false>,
+                                   dim3((unsigned)ctas), dim3(kThreads), 0, s, p, tpc);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -367,17 +367,15 @@ struct PageStream {
   uint32_t okbits;         // bit j % 32: page j of those in flight has a valid id
 
   // slice `split` of `nsplits` of the pages of positions [lo, hi); warp w takes pages
-  // pbeg + w + 8 j. steps: the pages of the slice's warp `warp & ~1`
-  __device__ __forceinline__ PageStream(const TreeParams& params, int split, int nsplits, int lo, int hi, uint8_t* ring, int& steps)
+  // pbeg + w + 8 j
+  __device__ __forceinline__ PageStream(const TreeParams& params, int split, int nsplits, int lo, int hi, uint8_t* ring)
       : p(params) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = lo / kPage, npages = hi > lo ? (hi - 1) / kPage - first + 1 : 0;
     const int chunk = (npages + nsplits - 1) / nsplits;
     const int pbeg = first + split * chunk, n = min(chunk, first + npages - pbeg);
-    auto count = [&](int w) { return n > w ? (n - w + kWarps - 1) / kWarps : 0; };
     begin = pbeg + warp;
-    nmine = count(warp);
-    steps = count(warp & ~1);
+    nmine = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
     off = (uint32_t)blockIdx.y * block_bytes(NG) + lane * 16;
     sring = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
     okbits = 0u;
@@ -433,8 +431,7 @@ __device__ void int2_part(const TreeParams& p, int b, int h, int tile, int split
   const float pscale = p.pv_scale[h], lg_ps = log2f(pscale);
   inv_ps = 1.f / pscale;
   uint8_t* ring = smem + warp * kStages * kBlockBytes;
-  int steps;
-  PageStream<NG> pages(p, split, nsplits, lo, hi, ring, steps);
+  PageStream<NG> pages(p, split, nsplits, lo, hi, ring);
 #pragma unroll
   for (int s = 0; s < kStages; ++s) pages.issue(s);
   __syncthreads();   // q~ fragments visible to every warp
@@ -1027,11 +1024,13 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_tree_pair_kernel(TreeParams
 // --------------------------------------------------------------------------
 // 3. merge: CTA x handles R query rows of (request z, KV head y): 16, the height of the
 //    un-rotation's product, or 4 when those would be few CTAs (the merge is then a chain
-//    of load latencies, and a quarter of the rows is four times the loads in flight)
+//    of load latencies, and a quarter of the rows is four times the loads in flight: whole
+//    calls of 160 and 832 rows 19.5 and 48.7 us against 21.3 and 51.3; of 4096 rows 174.8
+//    against 171.4)
 // --------------------------------------------------------------------------
 constexpr int kMergeThreads = 128;
 constexpr int kMergeRows = 16;
-constexpr int kMergeFewRows = 4096;   // rows of a call up to which the merge takes 4 rows a CTA
+constexpr int kMergeFewRows = 2048;   // rows of a call up to which the merge takes 4 rows a CTA
 
 template <int R>
 __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreeParams p) {
