@@ -170,6 +170,29 @@ def test_many_requests_bad_page_ids_and_replay():
     assert torch.equal(o[4], skipped) and torch.isfinite(o).all() and not torch.equal(o[4], good[4])
 
 
+@pytest.mark.parametrize("hq,hkv,batch", [(4, 2, 3), (16, 8, 10), (16, 2, 3)])
+def test_unused_rows_and_workspace_may_hold_anything(hq, hkv, batch):
+    # 22 (one wave and many requests) and 88 query rows per cached head
+    lengths, used = [300, 3, 130] + _MANY[3:batch], ([7, 11, 2] * 4)[:batch]
+    layer = _layer(lengths, hq, hkv, 4, 64, batch, 704, seed=28)
+    host, dev = draft(layer, batch, 11, 0)
+    par = torch.tensor([[-1] + [max(0, i - 1 - i % 3) for i in range(1, 11)]] * batch, dtype=torch.int32, device="cuda")
+    length = torch.tensor(used, dtype=torch.int32, device="cuda")
+    want = tree_call(layer, dev, par, length)
+    for b, n in enumerate(used):
+        par[b, n:] = 99
+        for x in dev:
+            x[b, n:] = float("nan")
+    size = layer.ctx.tree_attn_workspace_bytes(batch, 11)
+    for fill in (0xFF, 0x7F, 0):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        got = tree_call(layer, dev, par, length, workspace=ws)
+        for b, n in enumerate(used):
+            assert torch.isfinite(got[b, :n]).all() and torch.equal(got[b, :n], want[b, :n])
+            assert got[b, n:].isnan().all()
+    assert layer.ctx.error_flags() == 0
+
+
 def test_fold_rv():
     layer = _layer([400], 8, 2, 4, 64, 1, 512, seed=12, fold_rv=1)
     _check(layer, [400], 9, 2)
