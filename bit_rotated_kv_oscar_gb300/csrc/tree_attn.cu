@@ -1030,10 +1030,15 @@ __global__ void __launch_bounds__(kThreads, 2) oscar_tree_pair_kernel(TreeParams
 // --------------------------------------------------------------------------
 constexpr int kMergeThreads = 128;
 constexpr int kMergeRows = 16;
-constexpr int kMergeFewRows = 2048;   // rows of a call up to which the merge takes 4 rows a CTA
+constexpr int kMergeFewRows = 2048;     // rows of a call up to which the merge takes 4 rows a CTA
+constexpr int kMergeAheadRows = 304 * kMergeRows;   // and up to which two CTAs per SM hold them all
 
-template <int R>
-__global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreeParams p) {
+// AHEAD: the un-rotation operand is loaded before the wait. With more CTAs than two per SM its
+// 64 registers cost more than the loads: four CTAs per SM load it when they need it
+// (8 x 16k tokens, 488 rows: 487 us against 496; 16 ragged requests, 32 rows, 256 CTAs: 179
+// against 171)
+template <int R, bool AHEAD>
+__global__ void __launch_bounds__(kMergeThreads, AHEAD ? 1 : 4) oscar_tree_merge_kernel(TreeParams p) {
   constexpr int kPer = kMergeThreads / R;       // threads of a row
   constexpr int kVec = kHeadDim / 4 / kPer;     // float4 pieces of each
   extern __shared__ __align__(128) uint8_t smem[];
@@ -1046,7 +1051,7 @@ __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreePar
   // un-rotation operand, constant: warp w produces channels 32 w .. 32 w + 31,
   // out[n] = sum_k x[k] R_V[n][k]
   uint2 bf[4][8];
-  if (!p.fold_rv) {
+  auto load_rv = [&]() {
     const __half* rv = p.rv16 + (size_t)h * kHeadDim * kHeadDim;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt)
@@ -1055,7 +1060,8 @@ __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreePar
         const __half* src = rv + (32 * warp + 8 * nt + gid) * kHeadDim + 16 * kk + 2 * tig;
         bf[nt][kk] = make_uint2(*reinterpret_cast<const uint32_t*>(src), *reinterpret_cast<const uint32_t*>(src + 8));
       }
-  }
+  };
+  if (AHEAD && !p.fold_rv) load_rv();
   pdl_wait();
   pdl_trigger();
   const oscar_seq_state seq = p.state[b];
@@ -1147,6 +1153,7 @@ __global__ void __launch_bounds__(kMergeThreads) oscar_tree_merge_kernel(TreePar
                                                          f2_to_h2_bits(a2[4 * c + 2] * inv, a2[4 * c + 3] * inv));
     }
   }
+  if (!AHEAD && !p.fold_rv) load_rv();
   __syncthreads();
   float acc[4][4] = {};
   if (!p.fold_rv) {
@@ -1197,8 +1204,8 @@ cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t s) {
   static_assert(kRecUnit < kTreeRecWords, "query record");
   const int nslots = p.win_slots + p.splits, rows = p.nodes * p.gqa;
   const bool wide = p.tile_rows == 2 * kWideRows;
-  cudaError_t e = launch_pdl(wide ? oscar_tree_rotate_kernel<true> : oscar_tree_rotate_kernel<false>, dim3(p.row_tiles, p.num_kv_heads, p.batch), dim3(kRotThreads),
-                             kRotSmem, s, p);
+  cudaError_t e = launch_pdl(wide ? oscar_tree_rotate_kernel<true> : oscar_tree_rotate_kernel<false>,
+                             dim3(p.row_tiles, p.num_kv_heads, p.batch), dim3(kRotThreads), kRotSmem, s, p);
   if (e == cudaSuccess) {
     if (wide)
       e = launch_tree_wide(p, s);
@@ -1209,12 +1216,14 @@ cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t s) {
       e = launch_pdl(p.ngroups == kGroups ? oscar_tree_pair_kernel<kGroups> : oscar_tree_pair_kernel<2>,
                      dim3(2 * p.win_slots + p.splits, p.num_kv_heads, p.batch), dim3(kThreads), kPairSmem, s, p);
   }
-  if (e == cudaSuccess)
-    e = (int64_t)rows * p.num_kv_heads * p.batch <= kMergeFewRows
-            ? launch_pdl(oscar_tree_merge_kernel<4>, dim3((rows + 3) / 4, p.num_kv_heads, p.batch), dim3(kMergeThreads),
-                         nslots * 4 * 4, s, p)
-            : launch_pdl(oscar_tree_merge_kernel<kMergeRows>, dim3((rows + kMergeRows - 1) / kMergeRows, p.num_kv_heads, p.batch),
-                         dim3(kMergeThreads), nslots * kMergeRows * 4, s, p);
+  if (e == cudaSuccess) {
+    const int64_t all = (int64_t)rows * p.num_kv_heads * p.batch;
+    const int R = all <= kMergeFewRows ? 4 : kMergeRows;
+    e = launch_pdl(R == 4                    ? oscar_tree_merge_kernel<4, true>
+                   : all <= kMergeAheadRows ? oscar_tree_merge_kernel<kMergeRows, true>
+                                            : oscar_tree_merge_kernel<kMergeRows, false>,
+                   dim3((rows + R - 1) / R, p.num_kv_heads, p.batch), dim3(kMergeThreads), (size_t)nslots * R * 4, s, p);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -24,8 +24,9 @@
 // The BF16 part (sink, ring and the tree's own nodes) is the same computation in the raw
 // basis on bf16 operands; its probabilities are split into two bf16 parts.
 //
-// What bounds it: 8 requests x 16k tokens x 8 heads, 488 rows (two row tiles): 496 us (505
-// with two splits, of which 418 remain without the products); the tensor pipe alone would take 125 us at full
+// What bounds it: 8 requests x 16k tokens x 8 heads, 488 rows (two row tiles): 487 us with
+// rotation and merge, 425 alone (505 in all with two splits, of which 418 remain without the
+// products); the tensor pipe alone would take 125 us at full
 // rate, but a run of products of another shape or operand starts about 250 cycles after the
 // one before it, four times per row tile and 128 tokens. The rest is the softmax (a lane's
 // 128 exponentials, their sums and conversions, and the tensor-memory traffic) with eight

@@ -193,6 +193,15 @@ def test_unused_rows_and_workspace_may_hold_anything(hq, hkv, batch):
     assert layer.ctx.error_flags() == 0
 
 
+@pytest.mark.parametrize("fold", [0, 1])
+def test_many_rows(fold):
+    # 104 rows for each of 8 heads of 6 requests: the merge of more rows than two CTAs per SM
+    # hold at a time; some rows unused
+    lengths, used = [200, 68, 0, 133, 417, 90], [13, 13, 12, 13, 2, 13]
+    layer = _layer(lengths, 64, 8, 4, 64, 6, 448, seed=30, fold_rv=fold)
+    _check(layer, lengths, 13, 3, used)
+
+
 def test_fold_rv():
     layer = _layer([400], 8, 2, 4, 64, 1, 512, seed=12, fold_rv=1)
     _check(layer, [400], 9, 2)
